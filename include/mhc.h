@@ -387,6 +387,115 @@ MHC_API mhc_status mhc_depth_amax(int n, int64_t T, int L, const float *H, float
  */
 MHC_API mhc_status mhc_recompute_plan(int32_t n, int32_t L, int32_t *block, int64_t *resident);
 
+/*
+ * The layer function F of a transformer stack: layer norm and a gated
+ * feed-forward block.  An mHC layer hands h_in to F and merges f_out = F(h_in)
+ * back into the streams; F(h) = ffn(layer_norm(h)) is the feed-forward layer,
+ * and the two backward calls give its grad_h_in in training order.  The pages
+ * leave F open; these are the common definitions of its two parts.  As in
+ * mhc_backward, nothing of the forward is handed to the backward: it
+ * recomputes what it needs from x.
+ *
+ * The conventions at the top of this file hold, and: no output may overlap an
+ * input, another output or the workspace (MHC_ERR_INVALID_ARG).
+ */
+typedef struct mhc_norm_params {
+  int64_t T;      /* tokens, 1 <= T <= 2^31 - 257                              */
+  int64_t C;      /* channels, a multiple of 8, 8 <= C <= 2^24                 */
+  float eps;      /* added to the variance, >= 0                               */
+  int32_t dtype;  /* mhc_dtype of x, y and their gradients                     */
+} mhc_norm_params;
+
+/*
+ * mhc_layer_norm -- per token, over its C channels (statistics in float32,
+ * the variance about the mean, divided by C):
+ *   y[c] = (x[c] - mean) / sqrt(var + eps) * weight[c] + bias[c]
+ *
+ *   in : x [T][C] (dtype), weight [C] float32, bias [C] float32 or NULL (no bias)
+ *   out: y [T][C] (dtype)
+ * dev_status gets MHC_ERR_NONFINITE when a token's mean or 1/sqrt(var + eps)
+ * is not finite (a non-finite input, or a constant row with eps = 0); only
+ * that token's row of y is then undefined.  No workspace.
+ */
+MHC_API mhc_status mhc_layer_norm(const mhc_norm_params *p, const void *x, const float *weight,
+                                  const float *bias, void *y, int *dev_status,
+                                  mhc_stream_t stream);
+
+/*
+ * mhc_layer_norm_backward -- gradients of sum(grad_y . y), with the
+ * statistics recomputed from x: with xh = (x - mean) / sqrt(var + eps) and
+ * a = grad_y * weight,
+ *   grad_x[c]      = (a[c] - mean(a) - xh[c] mean(a xh)) / sqrt(var + eps)
+ *   grad_weight[c] = sum_t grad_y[t][c] xh[t][c],  grad_bias[c] = sum_t grad_y[t][c]
+ *
+ *   in : x, grad_y [T][C] (dtype), weight [C] float32
+ *   out: grad_x [T][C] (dtype), grad_weight [C], grad_bias [C] float32
+ *        (OVERWRITTEN with sums over the T tokens in a fixed order: repeated
+ *        calls give identical bits); grad_bias may be NULL.
+ * workspace: at least mhc_layer_norm_backward_workspace_size(p) bytes,
+ * 256-byte aligned; its contents on entry do not matter.  dev_status as in
+ * mhc_layer_norm (grad_weight then takes in the undefined row).
+ */
+MHC_API size_t mhc_layer_norm_backward_workspace_size(const mhc_norm_params *p);
+MHC_API mhc_status mhc_layer_norm_backward(const mhc_norm_params *p, const void *x,
+                                           const float *weight, const void *grad_y, void *grad_x,
+                                           float *grad_weight, float *grad_bias, void *workspace,
+                                           size_t workspace_bytes, int *dev_status,
+                                           mhc_stream_t stream);
+
+typedef enum mhc_activation {
+  MHC_ACT_SILU = 0,  /* g / (1 + exp(-g))                                      */
+  MHC_ACT_GELU = 1   /* g (1 + erf(g / sqrt 2)) / 2, the exact form            */
+} mhc_activation;
+
+typedef struct mhc_ffn_params {
+  int64_t T;        /* tokens, 1 <= T <= 2^31 - 257                            */
+  int64_t C;        /* channels in and out, a multiple of 8, 8 <= C <= 2^24    */
+  int64_t F;        /* hidden units, a multiple of 8, 8 <= F <= 2^24           */
+  int32_t dtype;    /* mhc_dtype of every tensor, the weights and their
+                       gradients included                                      */
+  int32_t act;      /* mhc_activation                                          */
+  int64_t wait_ns;  /* as in mhc_params                                        */
+} mhc_ffn_params;
+
+/*
+ * mhc_ffn -- the gated feed-forward block:
+ *   g = x w_gate^T,  u = x w_up^T,  a = act(g) * u,  y = a w_down^T
+ *
+ *   in : x [T][C], w_gate [F][C], w_up [F][C], w_down [C][F] (one row of
+ *        weights per output unit)
+ *   out: y [T][C]
+ * Sums run in float32.  With bf16 the product a is rounded to bf16 once
+ * between the two matrix products.  workspace: at least
+ * mhc_ffn_workspace_size(p) bytes, 256-byte aligned; its contents on entry do
+ * not matter.  Repeated calls give identical bits.
+ */
+MHC_API size_t mhc_ffn_workspace_size(const mhc_ffn_params *p);
+MHC_API mhc_status mhc_ffn(const mhc_ffn_params *p, const void *x, const void *w_gate,
+                           const void *w_up, const void *w_down, void *y, void *workspace,
+                           size_t workspace_bytes, int *dev_status, mhc_stream_t stream);
+
+/*
+ * mhc_ffn_backward -- gradients of sum(grad_y . y), with g and u recomputed:
+ *   da = grad_y w_down,  du = da act(g),  dg = da u act'(g)
+ *   grad_x = dg w_gate + du w_up
+ *   grad_w_gate = dg^T x,  grad_w_up = du^T x,  grad_w_down = grad_y^T a
+ *
+ *   in : x [T][C], w_gate, w_up [F][C], w_down [C][F], grad_y [T][C]
+ *   out: grad_x [T][C], grad_w_gate, grad_w_up [F][C], grad_w_down [C][F]
+ *        (OVERWRITTEN), all of the call's dtype
+ * Sums run in float32 and are rounded once at the end.  With bf16 the
+ * intermediates g, u, a, dg and du are rounded to bf16.  workspace: at least
+ * mhc_ffn_backward_workspace_size(p) bytes, 256-byte aligned; its contents on
+ * entry do not matter.  Repeated calls give identical bits.
+ */
+MHC_API size_t mhc_ffn_backward_workspace_size(const mhc_ffn_params *p);
+MHC_API mhc_status mhc_ffn_backward(const mhc_ffn_params *p, const void *x, const void *w_gate,
+                                    const void *w_up, const void *w_down, const void *grad_y,
+                                    void *grad_x, void *grad_w_gate, void *grad_w_up,
+                                    void *grad_w_down, void *workspace, size_t workspace_bytes,
+                                    int *dev_status, mhc_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -13,7 +13,10 @@ SYMBOLS = ("mhc_version", "mhc_status_string", "mhc_pre_workspace_size", "mhc_pr
            "mhc_backward_workspace_size", "mhc_backward", "mhc_backward_map", "mhc_backward_apply",
            "mhc_backward_noalloc", "mhc_post_backward", "mhc_pre_backward_workspace_size",
            "mhc_pre_backward", "mhc_post_fused_workspace_size", "mhc_post_fused",
-           "mhc_layer_input", "mhc_sinkhorn_knopp", "mhc_depth_amax", "mhc_recompute_plan")
+           "mhc_layer_input", "mhc_sinkhorn_knopp", "mhc_depth_amax", "mhc_recompute_plan",
+           "mhc_layer_norm", "mhc_layer_norm_backward_workspace_size", "mhc_layer_norm_backward",
+           "mhc_ffn_workspace_size", "mhc_ffn", "mhc_ffn_backward_workspace_size",
+           "mhc_ffn_backward")
 
 
 class MhcParams(ctypes.Structure):
@@ -21,6 +24,18 @@ class MhcParams(ctypes.Structure):
     _fields_ = [("n", ctypes.c_int32), ("t_max", ctypes.c_int32), ("T", ctypes.c_int64),
                 ("C", ctypes.c_int64), ("eps", ctypes.c_float), ("dtype", ctypes.c_int32),
                 ("alpha_groups", ctypes.c_int32), ("wait_ns", ctypes.c_int64)]
+
+
+class NormParams(ctypes.Structure):
+    """Mirror of ``mhc_norm_params`` in include/mhc.h."""
+    _fields_ = [("T", ctypes.c_int64), ("C", ctypes.c_int64), ("eps", ctypes.c_float),
+                ("dtype", ctypes.c_int32)]
+
+
+class FfnParams(ctypes.Structure):
+    """Mirror of ``mhc_ffn_params`` in include/mhc.h."""
+    _fields_ = [("T", ctypes.c_int64), ("C", ctypes.c_int64), ("F", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("wait_ns", ctypes.c_int64)]
 
 
 _lib = None
@@ -77,5 +92,20 @@ def load() -> ctypes.CDLL:
     lib.mhc_recompute_plan.argtypes = [ctypes.c_int32, ctypes.c_int32,
                                        ctypes.POINTER(ctypes.c_int32),
                                        ctypes.POINTER(ctypes.c_int64)]
+    np_, fp = ctypes.POINTER(NormParams), ctypes.POINTER(FfnParams)
+    lib.mhc_layer_norm.restype = i32
+    lib.mhc_layer_norm.argtypes = [np_, vp, vp, vp, vp, vp, vp]
+    lib.mhc_layer_norm_backward_workspace_size.restype = sz
+    lib.mhc_layer_norm_backward_workspace_size.argtypes = [np_]
+    lib.mhc_layer_norm_backward.restype = i32
+    lib.mhc_layer_norm_backward.argtypes = [np_, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp]
+    lib.mhc_ffn_workspace_size.restype = sz
+    lib.mhc_ffn_workspace_size.argtypes = [fp]
+    lib.mhc_ffn.restype = i32
+    lib.mhc_ffn.argtypes = [fp, vp, vp, vp, vp, vp, vp, sz, vp, vp]
+    lib.mhc_ffn_backward_workspace_size.restype = sz
+    lib.mhc_ffn_backward_workspace_size.argtypes = [fp]
+    lib.mhc_ffn_backward.restype = i32
+    lib.mhc_ffn_backward.argtypes = [fp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp]
     _lib = lib
     return lib

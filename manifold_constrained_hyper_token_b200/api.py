@@ -13,6 +13,7 @@ past the end of an allocation.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -418,3 +419,188 @@ def mhc_recompute_plan(n: int, L: int):
     st = _lib.load().mhc_recompute_plan(int(n), int(L), ctypes.byref(blk), ctypes.byref(res))
     _check(st, "mhc_recompute_plan")
     return int(blk.value), int(res.value)
+
+
+# ------------------------------------------- layer norm and feed-forward block
+ACT_CODE = {"silu": 0, "gelu": 1}
+
+
+def _shaped(t, shape, dtype, device, what):
+    """Reject a tensor of another shape or element type than the call's, on another
+    device, or laid out with gaps or in another order."""
+    if t.dtype != dtype:
+        raise ValueError(f"{what}: dtype {t.dtype}, the call takes {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, the call takes {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{what}: on {t.device}, the call runs on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: libmhc takes contiguous tensors only")
+
+
+def _rows(x, what="x"):
+    """(T, C) of an activation [T, C]."""
+    if x.dim() != 2:
+        raise ValueError(f"{what}: shape {tuple(x.shape)}, the call takes [T, C]")
+    if x.dtype not in DTYPE_CODE:
+        raise ValueError(f"unsupported activation dtype {x.dtype}")
+    return x.shape
+
+
+@contextlib.contextmanager
+def _on_stream(x, stream):
+    """x's device and the call's stream made current: tensors created inside belong to
+    that stream, and the launch goes to x's device whatever device was current.  Yields
+    the stream."""
+    if not x.is_cuda:
+        raise ValueError("libmhc takes CUDA tensors only")
+    s = torch.cuda.current_stream(x.device) if stream is None else stream
+    if s.device != x.device:
+        raise ValueError(f"stream: on {s.device}, the call runs on {x.device}")
+    with torch.cuda.stream(s):
+        yield s
+
+
+def _norm_params(x, eps):
+    T, C = _rows(x)
+    return _lib.NormParams(T=int(T), C=int(C), eps=float(eps), dtype=DTYPE_CODE[x.dtype])
+
+
+def mhc_layer_norm(x, weight, bias=None, *, eps: float = 1e-6, out=None, dev_status=None,
+                   stream=None):
+    """Layer norm over the last dimension: x [T,C], weight [C] fp32, bias [C] fp32 or None
+    -> y [T,C]."""
+    p = _norm_params(x, eps)
+    T, C = x.shape
+    _shaped(x, (T, C), x.dtype, x.device, "x")
+    _shaped(weight, (C,), F32, x.device, "weight")
+    if bias is not None:
+        _shaped(bias, (C,), F32, x.device, "bias")
+    if out is not None:
+        _shaped(out, (T, C), x.dtype, x.device, "out")
+    _fits(dev_status, 1, torch.int32, x.device, "dev_status")
+    with _on_stream(x, stream) as s:
+        y = torch.empty_like(x) if out is None else out
+        st = _lib.load().mhc_layer_norm(ctypes.byref(p), _p(x), _p(weight), _p(bias), _p(y),
+                                        _p(dev_status), _stream(s))
+    _check(st, "mhc_layer_norm")
+    return y
+
+
+def mhc_layer_norm_backward_workspace_size(T: int, C: int, dtype: torch.dtype) -> int:
+    if dtype not in DTYPE_CODE:
+        raise ValueError(f"unsupported activation dtype {dtype}")
+    p = _lib.NormParams(T=int(T), C=int(C), eps=0.0, dtype=DTYPE_CODE[dtype])
+    return int(_lib.load().mhc_layer_norm_backward_workspace_size(ctypes.byref(p)))
+
+
+def mhc_layer_norm_backward(x, weight, grad_y, *, eps: float = 1e-6, out=None, workspace=None,
+                            dev_status=None, stream=None):
+    """Gradients of mhc_layer_norm, the statistics recomputed from x.
+    Returns (grad_x [T,C], grad_weight [C] fp32, grad_bias [C] fp32)."""
+    p = _norm_params(x, eps)
+    T, C = x.shape
+    _shaped(x, (T, C), x.dtype, x.device, "x")
+    _shaped(weight, (C,), F32, x.device, "weight")
+    _shaped(grad_y, (T, C), x.dtype, x.device, "grad_y")
+    if out is not None:
+        for t, shape, dt, what in zip(out, ((T, C), (C,), (C,)), (x.dtype, F32, F32),
+                                      ("grad_x", "grad_weight", "grad_bias")):
+            _shaped(t, shape, dt, x.device, what)
+    _fits(dev_status, 1, torch.int32, x.device, "dev_status")
+    _on(workspace, x.device, "workspace")
+    lib = _lib.load()
+    with _on_stream(x, stream) as s:
+        if out is None:
+            out = (torch.empty_like(x), torch.empty(C, dtype=F32, device=x.device),
+                   torch.empty(C, dtype=F32, device=x.device))
+        gx, gw, gb = out
+        ws, wsb = _workspace(int(lib.mhc_layer_norm_backward_workspace_size(ctypes.byref(p))),
+                             x.device, workspace)
+        st = lib.mhc_layer_norm_backward(ctypes.byref(p), _p(x), _p(weight), _p(grad_y), _p(gx),
+                                         _p(gw), _p(gb), _p(ws), wsb, _p(dev_status), _stream(s))
+    _check(st, "mhc_layer_norm_backward")
+    return gx, gw, gb
+
+
+def _ffn_params(T, C, F, dtype, act="silu", wait_ns=0):
+    if dtype not in DTYPE_CODE:
+        raise ValueError(f"unsupported activation dtype {dtype}")
+    if act not in ACT_CODE:
+        raise ValueError(f"act: {act!r}, the call takes one of {sorted(ACT_CODE)}")
+    return _lib.FfnParams(T=int(T), C=int(C), F=int(F), dtype=DTYPE_CODE[dtype],
+                          act=ACT_CODE[act], wait_ns=int(wait_ns))
+
+
+def mhc_ffn_workspace_size(T: int, C: int, F: int, dtype: torch.dtype) -> int:
+    p = _ffn_params(T, C, F, dtype)
+    return int(_lib.load().mhc_ffn_workspace_size(ctypes.byref(p)))
+
+
+def mhc_ffn_backward_workspace_size(T: int, C: int, F: int, dtype: torch.dtype) -> int:
+    p = _ffn_params(T, C, F, dtype)
+    return int(_lib.load().mhc_ffn_backward_workspace_size(ctypes.byref(p)))
+
+
+def _ffn_weights(x, w_gate, w_up, w_down):
+    """F, after checking x [T,C], w_gate and w_up [F,C], w_down [C,F]."""
+    T, C = _rows(x)
+    if w_gate.dim() != 2:
+        raise ValueError(f"w_gate: shape {tuple(w_gate.shape)}, the call takes [F, {C}]")
+    F = w_gate.shape[0]
+    _shaped(x, (T, C), x.dtype, x.device, "x")
+    _shaped(w_gate, (F, C), x.dtype, x.device, "w_gate")
+    _shaped(w_up, (F, C), x.dtype, x.device, "w_up")
+    _shaped(w_down, (C, F), x.dtype, x.device, "w_down")
+    return F
+
+
+def mhc_ffn(x, w_gate, w_up, w_down, *, act: str = "silu", wait_ns: int = 0, out=None,
+            workspace=None, dev_status=None, stream=None):
+    """Gated feed-forward block: x [T,C], w_gate and w_up [F,C], w_down [C,F], act "silu" or
+    "gelu" -> y [T,C] = (act(x w_gate^T) * (x w_up^T)) w_down^T."""
+    F = _ffn_weights(x, w_gate, w_up, w_down)
+    T, C = x.shape
+    p = _ffn_params(T, C, F, x.dtype, act, wait_ns)
+    if out is not None:
+        _shaped(out, (T, C), x.dtype, x.device, "out")
+    _fits(dev_status, 1, torch.int32, x.device, "dev_status")
+    _on(workspace, x.device, "workspace")
+    lib = _lib.load()
+    with _on_stream(x, stream) as s:
+        y = torch.empty_like(x) if out is None else out
+        ws, wsb = _workspace(int(lib.mhc_ffn_workspace_size(ctypes.byref(p))), x.device,
+                             workspace)
+        st = lib.mhc_ffn(ctypes.byref(p), _p(x), _p(w_gate), _p(w_up), _p(w_down), _p(y), _p(ws),
+                         wsb, _p(dev_status), _stream(s))
+    _check(st, "mhc_ffn")
+    return y
+
+
+def mhc_ffn_backward(x, w_gate, w_up, w_down, grad_y, *, act: str = "silu", wait_ns: int = 0,
+                     out=None, workspace=None, dev_status=None, stream=None):
+    """Gradients of mhc_ffn, the two projections recomputed from x.
+    Returns (grad_x [T,C], grad_w_gate [F,C], grad_w_up [F,C], grad_w_down [C,F])."""
+    F = _ffn_weights(x, w_gate, w_up, w_down)
+    T, C = x.shape
+    p = _ffn_params(T, C, F, x.dtype, act, wait_ns)
+    _shaped(grad_y, (T, C), x.dtype, x.device, "grad_y")
+    if out is not None:
+        for t, shape, what in zip(out, ((T, C), (F, C), (F, C), (C, F)),
+                                  ("grad_x", "grad_w_gate", "grad_w_up", "grad_w_down")):
+            _shaped(t, shape, x.dtype, x.device, what)
+    _fits(dev_status, 1, torch.int32, x.device, "dev_status")
+    _on(workspace, x.device, "workspace")
+    lib = _lib.load()
+    with _on_stream(x, stream) as s:
+        if out is None:
+            out = (torch.empty_like(x), torch.empty_like(w_gate), torch.empty_like(w_up),
+                   torch.empty_like(w_down))
+        gx, gwg, gwu, gwd = out
+        ws, wsb = _workspace(int(lib.mhc_ffn_backward_workspace_size(ctypes.byref(p))), x.device,
+                             workspace)
+        st = lib.mhc_ffn_backward(ctypes.byref(p), _p(x), _p(w_gate), _p(w_up), _p(w_down),
+                                  _p(grad_y), _p(gx), _p(gwg), _p(gwu), _p(gwd), _p(ws), wsb,
+                                  _p(dev_status), _stream(s))
+    _check(st, "mhc_ffn_backward")
+    return gx, gwg, gwu, gwd

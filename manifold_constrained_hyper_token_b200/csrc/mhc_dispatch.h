@@ -171,4 +171,24 @@ cudaError_t apply_dispatch(int n, int dtype, int64_t T, int64_t C, const void* x
                            int nparts, void* gx, void* gf, float* gphi, float* gb, float* ga,
                            int ag, cudaStream_t s);
 
+// k_norm.cu: layer norm over a token's C channels (b and gb may be null)
+cudaError_t norm_fwd_dispatch(int dtype, int64_t rows, int64_t C, float eps, const void* x,
+                              const float* w, const float* b, void* y, int* st, cudaStream_t s);
+cudaError_t norm_bwd_dispatch(int dtype, int64_t rows, int64_t C, float eps, const void* x,
+                              const float* w, const void* gy, void* gx, float* gw, float* gb,
+                              void* ws, int* st, cudaStream_t s);
+size_t norm_bwd_workspace_bytes(int64_t rows, int64_t C, int dtype);
+
+// k_ffn.cu: the gated feed-forward block of t tokens, C channels and F hidden
+// units; ws holds the matching *_workspace_bytes()
+cudaError_t ffn_fwd_dispatch(int dtype, int act, int64_t t, int64_t C, int64_t F, const void* x,
+                             const void* wg, const void* wu, const void* wd, void* y, void* ws,
+                             int* st, int64_t wait_ns, cudaStream_t s);
+cudaError_t ffn_bwd_dispatch(int dtype, int act, int64_t t, int64_t C, int64_t F, const void* x,
+                             const void* wg, const void* wu, const void* wd, const void* gy,
+                             void* gx, void* gwg, void* gwu, void* gwd, void* ws, int* st,
+                             int64_t wait_ns, cudaStream_t s);
+size_t ffn_fwd_workspace_bytes(int dtype, int64_t t, int64_t C, int64_t F);
+size_t ffn_bwd_workspace_bytes(int dtype, int64_t t, int64_t C, int64_t F);
+
 }  // namespace mhc

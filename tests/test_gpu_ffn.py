@@ -1,0 +1,212 @@
+"""The gated feed-forward block on the GPU against fp64.
+
+Every element is held to the bound that layer_reference propagates (rigorous, so it grows
+with the length of the sums); bf16 results also to the 2-norm: each stored value is off by
+at most 2^-8 of itself, independently, and a result sees at most four such roundings on its
+way (g or u, then a, dg or du, then itself), so |error| <= sqrt(4) 2^-8 |result|.
+"""
+import pytest
+import torch
+
+import layer_reference as R
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+TIMEOUT = 5
+GRADS = ("grad_x", "grad_w_gate", "grad_w_up", "grad_w_down")
+
+
+@pytest.fixture(scope="module")
+def mhc():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from manifold_constrained_hyper_token_b200 import build
+    build.build()
+    import manifold_constrained_hyper_token_b200 as m
+    return m
+
+
+def _case(T, C, F, dtype, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    n = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    return ((1.5 * n(T, C)).to(dtype), (n(F, C) * C ** -0.5).to(dtype),
+            (n(F, C) * C ** -0.5).to(dtype), (n(C, F) * F ** -0.5).to(dtype), n(T, C).to(dtype))
+
+
+def _check_fwd(y, x, wg, wu, wd, act, dtype):
+    ref = R.ffn(x, wg, wu, wd, act)
+    R.assert_within(y, ref, R.ffn_bound(x, wg, wu, wd, act, dtype), "y")
+    if dtype == BF16:
+        assert R.norm_rel(y, ref) < 2.0 ** -7
+
+
+def _check_bwd(got, x, wg, wu, wd, gy, act, dtype):
+    ref = R.ffn_grad(x, wg, wu, wd, gy, act)
+    bnd = R.ffn_grad_bound(x, wg, wu, wd, gy, act, dtype)
+    for g, r, b, name in zip(got, ref, bnd, GRADS):
+        R.assert_within(g, r, b, name)
+        if dtype == BF16:
+            assert R.norm_rel(g, r) < 2.0 ** -7, name
+
+
+# (T, C, F): one element blocks, single tokens, widths that end inside every tile, each side
+# of 64, 128 and 256 tokens, several tiles in every direction
+SHAPES = [(1, 8, 8), (1, 64, 64), (1, 512, 1368), (2, 72, 200), (3, 1000, 264), (8, 256, 512),
+          (15, 136, 1032), (16, 520, 248), (17, 64, 2048), (31, 328, 136), (33, 128, 128),
+          (48, 1024, 264), (63, 200, 392), (64, 256, 256), (65, 264, 520), (100, 72, 8),
+          (127, 8, 1000), (128, 512, 512), (129, 136, 264), (130, 512, 1368), (200, 1032, 96),
+          (255, 320, 184), (256, 256, 1024), (257, 264, 776), (300, 1288, 648), (513, 520, 1032),
+          (777, 64, 72), (1025, 384, 520)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,C,F", SHAPES)
+def test_ffn(mhc, T, C, F, dtype):
+    x, wg, wu, wd, _ = _case(T, C, F, dtype, T * 7 + C + F)
+    for act in ("silu", "gelu"):
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        y = mhc.mhc_ffn(x, wg, wu, wd, act=act, dev_status=st)
+        assert int(st.item()) == 0
+        _check_fwd(y, x, wg, wu, wd, act, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,C,F", SHAPES)
+def test_ffn_backward(mhc, T, C, F, dtype):
+    x, wg, wu, wd, gy = _case(T, C, F, dtype, T * 7 + C + F)
+    for act in ("silu", "gelu"):
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = mhc.mhc_ffn_backward(x, wg, wu, wd, gy, act=act, dev_status=st)
+        assert int(st.item()) == 0
+        _check_bwd(got, x, wg, wu, wd, gy, act, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,C,F", [(1, 4096, 8200), (40, 7168, 1024), (1500, 1000, 2728),
+                                   (5000, 264, 520), (2100, 2056, 1032)])
+def test_larger(mhc, T, C, F, dtype):
+    """Long sums in each direction, and more tiles than SMs."""
+    x, wg, wu, wd, gy = _case(T, C, F, dtype, 5)
+    _check_fwd(mhc.mhc_ffn(x, wg, wu, wd), x, wg, wu, wd, "silu", dtype)
+    _check_bwd(mhc.mhc_ffn_backward(x, wg, wu, wd, gy), x, wg, wu, wd, gy, "silu", dtype)
+
+
+@pytest.mark.parametrize("T", [3, 300])
+def test_saturated_gates(mhc, T):
+    """Gates of several hundred either way: the activation's limits, without overflow."""
+    x, wg, wu, wd, gy = _case(T, 64, 96, F32, 9)
+    wg = wg * 200
+    for act in ("silu", "gelu"):
+        _check_fwd(mhc.mhc_ffn(x, wg, wu, wd, act=act), x, wg, wu, wd, act, F32)
+        _check_bwd(mhc.mhc_ffn_backward(x, wg, wu, wd, gy, act=act), x, wg, wu, wd, gy, act, F32)
+        b = [t.to(BF16) for t in (x, wg, wu, wd, gy)]
+        y = mhc.mhc_ffn(*b[:4], act=act)
+        ref = R.ffn(*b[:4], act)
+        R.assert_within(y, ref, R.ffn_bound(*b[:4], act, BF16), "y")
+        for g, r, d, n in zip(mhc.mhc_ffn_backward(*b, act=act), R.ffn_grad(*b, act),
+                              R.ffn_grad_bound(*b, act, BF16), GRADS):
+            R.assert_within(g, r, d, n)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,C,F", [(5, 136, 200), (100, 136, 200), (300, 136, 392)])
+def test_nonfinite_tokens_stay_alone(mhc, T, C, F, dtype):
+    """A token that is not finite spoils its own rows of y and grad_x and no others."""
+    x, wg, wu, wd, gy = _case(T, C, F, dtype, 4)
+    bad = x.clone()
+    bad[2, 5] = float("nan")
+    bad[T - 1, 0] = float("inf")
+    keep = [t for t in range(T) if t not in (2, T - 1)]
+    y, want = mhc.mhc_ffn(bad, wg, wu, wd), mhc.mhc_ffn(x, wg, wu, wd)
+    assert torch.equal(y[keep], want[keep])
+    assert bool(y[2].isnan().all()) and not bool(y[T - 1].isfinite().any())
+    gx = mhc.mhc_ffn_backward(bad, wg, wu, wd, gy)[0]
+    want = mhc.mhc_ffn_backward(x, wg, wu, wd, gy)[0]
+    assert torch.equal(gx[keep], want[keep]) and bool(gx[2].isnan().all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,C,F", [(1, 136, 264), (33, 264, 520), (300, 520, 264)])
+def test_repeats_bit_for_bit_and_writes_nothing_else(mhc, T, C, F, dtype):
+    x, wg, wu, wd, gy = _case(T, C, F, dtype, 6)
+    nf = mhc.mhc_ffn_workspace_size(T, C, F, dtype)
+    nb = mhc.mhc_ffn_backward_workspace_size(T, C, F, dtype)
+    first = None
+    for fill in (0, 255):
+        y, gx = (torch.full((T + 2, C), 7.0, dtype=dtype, device="cuda") for _ in range(2))
+        gwg, gwu = (torch.full((F + 2, C), 7.0, dtype=dtype, device="cuda") for _ in range(2))
+        gwd = torch.full((C + 2, F), 7.0, dtype=dtype, device="cuda")
+        ws = torch.full((max(nf, nb) + 256,), fill, dtype=torch.uint8, device="cuda")
+        mhc.mhc_ffn(x, wg, wu, wd, out=y[1:-1], workspace=ws[:nf])
+        mhc.mhc_ffn_backward(x, wg, wu, wd, gy, workspace=ws[:nb],
+                             out=tuple(t[1:-1] for t in (gx, gwg, gwu, gwd)))
+        for t in (y, gx, gwg, gwu, gwd):
+            assert bool((t[0] == 7).all()) and bool((t[-1] == 7).all())
+        assert bool((ws[max(nf, nb):] == fill).all())
+        out = [t.cpu() for t in (y, gx, gwg, gwu, gwd)]
+        assert first is None or all(torch.equal(a, c) for a, c in zip(first, out))
+        first = out
+
+
+def test_a_token_does_not_depend_on_its_batch(mhc):
+    """Rows of a larger batch agree with the same rows alone, to the roundings."""
+    x, wg, wu, wd, _ = _case(700, 264, 520, BF16, 8)
+    whole = mhc.mhc_ffn(x, wg, wu, wd)
+    for n in (1, 5, 64, 130, 256):
+        _check_fwd(mhc.mhc_ffn(x[:n], wg, wu, wd), x[:n], wg, wu, wd, "silu", BF16)
+        assert R.norm_rel(mhc.mhc_ffn(x[:n], wg, wu, wd), whole[:n].double()) < 2.0 ** -7
+
+
+@pytest.mark.parametrize("T", [1, 200])
+def test_other_stream_and_graphs_with_one_workspace(mhc, T):
+    """On another stream than the current one; and two graphs that share a workspace, replayed
+    one after the other on new inputs."""
+    C, F = 264, 520
+    x, wg, wu, wd, gy = _case(T, C, F, BF16, 10)
+    want = mhc.mhc_ffn(x, wg, wu, wd), *mhc.mhc_ffn_backward(x, wg, wu, wd, gy)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = (mhc.mhc_ffn(x, wg, wu, wd, stream=s),
+           *mhc.mhc_ffn_backward(x, wg, wu, wd, gy, stream=s))
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    n = max(mhc.mhc_ffn_workspace_size(T, C, F, BF16),
+            mhc.mhc_ffn_backward_workspace_size(T, C, F, BF16))
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    xs, gs = torch.zeros_like(x), torch.zeros_like(gy)
+    gf, gb = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gf):
+        y = mhc.mhc_ffn(xs, wg, wu, wd, workspace=ws)
+    with torch.cuda.graph(gb):
+        grads = mhc.mhc_ffn_backward(xs, wg, wu, wd, gs, workspace=ws)
+    for scale in (1.0, 0.5, 1.0):
+        xs.copy_(x * scale)
+        gs.copy_(gy)
+        gf.replay()
+        gb.replay()
+        gf.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, (y, *grads)))
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_gradients_against_differences(mhc, act):
+    """fp32: grad . d against central differences of sum(gy . y) along random d.  With h = 2^-6
+    the difference's own error is h^2 times a third derivative (of order one per unit of d's
+    norm, the steps being h d with |d| = 1) and the forward's rounding over h: 2^-24 * 64 * 30
+    |y| |gy|.  Both stay below 2e-4 of |gy| |y|."""
+    x, wg, wu, wd, gy = _case(40, 72, 136, F32, 11)
+    grads = mhc.mhc_ffn_backward(x, wg, wu, wd, gy, act=act)
+    args, h = (x, wg, wu, wd), 2.0 ** -6
+    y = mhc.mhc_ffn(*args, act=act).double()
+    for i, g in enumerate(grads):
+        d = torch.randn(args[i].shape, generator=torch.Generator().manual_seed(i)).cuda()
+        d /= d.norm()
+        up, dn = list(args), list(args)
+        up[i], dn[i] = args[i] + h * d, args[i] - h * d
+        step = (up[i].double() - dn[i].double())  # the step as rounded
+        diff = (mhc.mhc_ffn(*up, act=act).double() - mhc.mhc_ffn(*dn, act=act).double())
+        got = float((diff * gy.double()).sum()) / (2 * h)
+        want = float((g.double() * step).sum()) / (2 * h)
+        assert abs(got - want) <= 2e-4 * float(gy.norm()) * float(y.norm()), GRADS[i]

@@ -1,0 +1,170 @@
+"""Layer norm on the GPU against fp64, element by element within the bounds of
+layer_reference, at widths on both sides of every layout the kernels choose (a row per
+warp, a row per CTA, rows longer than the registers of a CTA)."""
+import pytest
+import torch
+
+import layer_reference as R
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+NONFINITE = 4
+
+
+@pytest.fixture(scope="module")
+def mhc():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from manifold_constrained_hyper_token_b200 import build
+    build.build()
+    import manifold_constrained_hyper_token_b200 as m
+    return m
+
+
+def _case(T, C, dtype, seed):
+    g = torch.Generator().manual_seed(seed)
+    n = lambda *s: torch.randn(*s, generator=g)
+    x = (n(T, C) * (torch.rand(T, 1, generator=g) * 3 + 0.1) + n(T, 1)).to(dtype)
+    return x, 1 + 0.3 * n(C), 0.3 * n(C), n(T, C).to(dtype)
+
+
+SHAPES = [(1, 8), (3, 16), (1, 256), (9, 264), (130, 512), (17, 1000), (5, 1024), (33, 1032),
+          (7, 2056), (300, 4096), (4, 4104), (2, 7168), (301, 7168), (3, 8200), (2, 16384),
+          (3, 16392), (2, 32776), (70, 40000), (1, 100000)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,C", SHAPES)
+def test_norm(mhc, T, C, dtype):
+    x, w, b, _ = _case(T, C, dtype, T + C)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for bias in (b, None):
+        y = mhc.mhc_layer_norm(x.cuda(), w.cuda(), None if bias is None else b.cuda(),
+                               dev_status=st)
+        R.assert_within(y, R.norm(x, w, bias, 1e-6), R.norm_bound(x, w, bias, 1e-6, dtype), "y")
+    assert int(st.item()) == 0
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,C", SHAPES + [(5000, 64), (1999, 1024), (700, 2048), (401, 12288)])
+def test_norm_backward(mhc, T, C, dtype):
+    x, w, _, gy = _case(T, C, dtype, T + C)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = mhc.mhc_layer_norm_backward(x.cuda(), w.cuda(), gy.cuda(), dev_status=st)
+    ref, bound = R.norm_grad(x, w, gy, 1e-6), R.norm_grad_bound(x, w, gy, 1e-6, dtype)
+    for g, r, d, name in zip(got, ref, bound, ("grad_x", "grad_weight", "grad_bias")):
+        R.assert_within(g, r, d, name)
+    assert int(st.item()) == 0
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,C", [(4, 64), (3, 2048), (2, 40000)])
+def test_rows_far_from_zero(mhc, T, C, dtype):
+    """Mean 300 times the deviation: the variance is taken about the mean."""
+    g = torch.Generator().manual_seed(C)
+    x = (300 + torch.randn(T, C, generator=g)).to(dtype)
+    w, gy = torch.ones(C), torch.randn(T, C, generator=g).to(dtype)
+    y = mhc.mhc_layer_norm(x.cuda(), w.cuda())
+    R.assert_within(y, R.norm(x, w, None, 1e-6), R.norm_bound(x, w, None, 1e-6, dtype), "y")
+    got = mhc.mhc_layer_norm_backward(x.cuda(), w.cuda(), gy.cuda())
+    for a, r, d, n in zip(got, R.norm_grad(x, w, gy, 1e-6),
+                          R.norm_grad_bound(x, w, gy, 1e-6, dtype), ("gx", "gw", "gb")):
+        R.assert_within(a, r, d, n)
+
+
+@pytest.mark.parametrize("C", [64, 2048, 40000])
+def test_constant_rows(mhc, C):
+    """A constant row has no deviation: y is the bias, and grad_x the centred a / sqrt(eps)."""
+    x = torch.full((3, C), 2.0)
+    w, b = torch.full((C,), 1.5), torch.linspace(-1, 1, C)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = mhc.mhc_layer_norm(x.cuda(), w.cuda(), b.cuda(), eps=1e-4, dev_status=st)
+    assert torch.equal(y.cpu(), b.expand(3, C)) and int(st.item()) == 0
+    mhc.mhc_layer_norm(x.cuda(), w.cuda(), b.cuda(), eps=0.0, dev_status=st)
+    assert int(st.item()) == NONFINITE
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("C", [64, 1032, 40000])
+def test_nonfinite_rows_stay_alone(mhc, C, dtype, bad):
+    x, w, b, gy = _case(5, C, dtype, C)
+    x[2, C // 2] = bad
+    keep = [0, 1, 3, 4]
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = mhc.mhc_layer_norm(x.cuda(), w.cuda(), b.cuda(), dev_status=st).cpu()
+    assert int(st.item()) == NONFINITE
+    R.assert_within(y[keep], R.norm(x[keep], w, b, 1e-6),
+                    R.norm_bound(x[keep], w, b, 1e-6, dtype), "y")
+    st.zero_()
+    gx = mhc.mhc_layer_norm_backward(x.cuda(), w.cuda(), gy.cuda(), dev_status=st)[0].cpu()
+    assert int(st.item()) == NONFINITE
+    R.assert_within(gx[keep], R.norm_grad(x[keep], w, gy[keep], 1e-6)[0],
+                    R.norm_grad_bound(x[keep], w, gy[keep], 1e-6, dtype)[0], "grad_x")
+
+
+@pytest.mark.parametrize("T,C", [(1000, 64), (777, 7168), (70, 40000)])
+def test_repeats_bit_for_bit_and_writes_nothing_else(mhc, T, C):
+    x, w, b, gy = _case(T, C, BF16, 3)
+    xd, wd, bd, gd = x.cuda(), w.cuda(), b.cuda(), gy.cuda()
+    n = mhc.mhc_layer_norm_backward_workspace_size(T, C, BF16)
+    first = None
+    for fill in (0, 255):
+        # outputs inside larger buffers: the rows around them keep their bytes
+        y = torch.full((T + 2, C), 7.0, dtype=BF16, device="cuda")
+        gx = y.clone()
+        gwb = torch.full((4, C), 7.0, device="cuda")
+        ws = torch.full((n + 256,), fill, dtype=torch.uint8, device="cuda")
+        mhc.mhc_layer_norm(xd, wd, bd, out=y[1:-1])
+        mhc.mhc_layer_norm_backward(xd, wd, gd, out=(gx[1:-1], gwb[1], gwb[2]), workspace=ws[:n])
+        for t in (y, gx, gwb):
+            assert bool((t[0] == 7).all()) and bool((t[-1] == 7).all())
+        assert bool((ws[n:] == fill).all())
+        out = [t.cpu() for t in (y, gx, gwb)]
+        assert first is None or all(torch.equal(a, c) for a, c in zip(first, out))
+        first = out
+
+
+def test_other_stream_and_graph(mhc):
+    """The call runs on the stream it is given; captured calls replay on new inputs."""
+    T, C = 600, 1024
+    x, w, b, gy = (t.cuda() for t in _case(T, C, BF16, 5))
+    want = mhc.mhc_layer_norm(x, w, b), *mhc.mhc_layer_norm_backward(x, w, gy)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = mhc.mhc_layer_norm(x, w, b, stream=s), *mhc.mhc_layer_norm_backward(x, w, gy, stream=s)
+    s.synchronize()
+    assert all(torch.equal(a, c) for a, c in zip(want, got))
+    xs, gs = torch.zeros_like(x), torch.zeros_like(gy)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = mhc.mhc_layer_norm(xs, w, b)
+        grads = mhc.mhc_layer_norm_backward(xs, w, gs)
+    for _ in range(2):
+        xs.copy_(x)
+        gs.copy_(gy)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, c) for a, c in zip(want, (y, *grads)))
+
+
+def test_largest_offsets(mhc):
+    """More than 2^31 elements: the last rows are addressed in 64 bits."""
+    T, C = 70000, 32768
+    if torch.cuda.get_device_properties(0).total_memory < 40 << 30:
+        pytest.skip("needs 15 GB")
+    x = torch.zeros(T, C, dtype=BF16, device="cuda")
+    g = torch.Generator().manual_seed(0)
+    last = torch.randn(4, C, generator=g).to(BF16)
+    x[-4:] = last.cuda()
+    w, b = torch.ones(C), torch.zeros(C)
+    y = mhc.mhc_layer_norm(x, w.cuda(), b.cuda())
+    R.assert_within(y[-4:], R.norm(last, w, b, 1e-6), R.norm_bound(last, w, b, 1e-6, BF16), "y")
+    assert bool((y[:8] == 0).all())
+    gx, gw, gb = mhc.mhc_layer_norm_backward(x, w.cuda(), x)
+    ref = R.norm_grad(last, w, last, 1e-6)
+    bnd = R.norm_grad_bound(last, w, last, 1e-6, BF16)
+    R.assert_within(gx[-4:], ref[0], bnd[0], "grad_x")
+    R.assert_within(gw, ref[1], bnd[1], "grad_weight")
+    R.assert_within(gb, ref[2], bnd[2], "grad_bias")
