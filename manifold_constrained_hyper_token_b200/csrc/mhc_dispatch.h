@@ -179,7 +179,7 @@ cudaError_t norm_bwd_dispatch(int dtype, int64_t rows, int64_t C, float eps, con
                               void* ws, int* st, cudaStream_t s);
 size_t norm_bwd_workspace_bytes(int64_t rows, int64_t C, int dtype);
 
-// k_ffn.cu: the gated feed-forward block of t tokens, C channels and F hidden
+// k_ffn_tc.cu: the gated feed-forward block of t tokens, C channels and F hidden
 // units; ws holds the matching *_workspace_bytes()
 cudaError_t ffn_fwd_dispatch(int dtype, int act, int64_t t, int64_t C, int64_t F, const void* x,
                              const void* wg, const void* wu, const void* wd, void* y, void* ws,

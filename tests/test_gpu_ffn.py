@@ -210,3 +210,30 @@ def test_gradients_against_differences(mhc, act):
         got = float((diff * gy.double()).sum()) / (2 * h)
         want = float((g.double() * step).sum()) / (2 * h)
         assert abs(got - want) <= 2e-4 * float(gy.norm()) * float(y.norm()), GRADS[i]
+
+
+@pytest.mark.parametrize("T,C,F", [(300, 264, 520), (40, 264, 520), (1500, 1032, 2056)])
+@pytest.mark.parametrize("backward", [False, True])
+def test_times_out_then_recovers(mhc, T, C, F, backward):
+    """A wait limit of 1 ns makes the kernels' waits give up: the status word says so, and an
+    ordinary call on the same buffers and workspace is right again."""
+    x, wg, wu, wd, gy = _case(T, C, F, BF16, 12)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    if backward:
+        ws = torch.empty(mhc.mhc_ffn_backward_workspace_size(T, C, F, BF16), dtype=torch.uint8,
+                         device="cuda")
+        mhc.mhc_ffn_backward(x, wg, wu, wd, gy, workspace=ws, dev_status=st, wait_ns=1)
+        assert int(st.item()) == TIMEOUT
+        st.zero_()
+        got = mhc.mhc_ffn_backward(x, wg, wu, wd, gy, workspace=ws, dev_status=st)
+        assert int(st.item()) == 0
+        _check_bwd(got, x, wg, wu, wd, gy, "silu", BF16)
+    else:
+        ws = torch.empty(mhc.mhc_ffn_workspace_size(T, C, F, BF16), dtype=torch.uint8,
+                         device="cuda")
+        mhc.mhc_ffn(x, wg, wu, wd, workspace=ws, dev_status=st, wait_ns=1)
+        assert int(st.item()) == TIMEOUT
+        st.zero_()
+        y = mhc.mhc_ffn(x, wg, wu, wd, workspace=ws, dev_status=st)
+        assert int(st.item()) == 0
+        _check_fwd(y, x, wg, wu, wd, "silu", BF16)
