@@ -9,18 +9,22 @@
 //   EPI_KEEP   the same, and g and u themselves (the backward's recompute)
 //   EPI_DGATE  D = da: reads g and u, writes dg = da u act'(g), du = da act(g)
 //
-// Two CTAs (a cluster, one CTA per SM) make one 256 x 256 tile with paired
-// MMAs (cta_group::2, 256 x 256 x 16): each brings 128 rows of A and 128 of B
-// per 64-wide k block into a six-stage ring by TMA (32 KB a stage and CTA) and
-// holds 128 rows of D in its TMEM, so an SM reads 64 bytes of operands from L2
-// per 8192 multiply-adds where a single-CTA 128 x 256 tile would read 96.  Two
-// accumulators (all 512 TMEM columns) let the epilogue of one tile run under the
-// products of the next.  Tiles go over the pairs in bands of eight row tiles, so
-// that the tiles in flight share operands in L2.
+// Two CTAs (a cluster, one CTA per SM) make one 256 x TN tile with paired MMAs
+// (cta_group::2, 256 x TN x 16): each brings 128 rows of A and TN / 2 of B per
+// 64-wide k block into a six-stage ring by TMA and holds 128 rows of D in its
+// TMEM.  With TN = 256 an SM reads 64 bytes of operands from L2 per 8192
+// multiply-adds where a single-CTA 128 x 256 tile would read 96.  Two
+// accumulators let the epilogue of one tile run under the products of the next.
+// Tiles go over the pairs in bands of eight row tiles, so that the tiles in
+// flight share operands in L2.
 //
-// fp32 operands come as three bf16 planes each (their exact split, split3);
-// the six products of planes whose sum of orders is at most two are taken in one
-// accumulator, the smallest first.  What is left out is below 2^-25 of a product.
+// fp32 operands come as three bf16 planes each (their exact split, split3); the
+// six products of planes whose orders add up to at most two are taken, the
+// smallest first, and what is left out is below 2^-25 of a product.  The tensor
+// cores' adder cuts instead of rounding, about half a unit of the last place per
+// 16-wide step, which adds up over a long sum (measured: 137 x 2^-24 at k =
+// 5456).  So the fp32 sums leave the accumulator every kChunk k blocks and are
+// added up, rounded, in a third TMEM region.
 //
 // Warps of a CTA: 0 TMA; 1 the MMAs (first CTA only); 2 TMEM; 4-7 the epilogue.
 // Both CTAs' copies complete on the first CTA's barriers.  (A thread of the
@@ -29,25 +33,34 @@
 // Every wait is bounded as in the other tensor-core kernels: on timeout the
 // kernel records MHC_ERR_TIMEOUT, drains what it issued and returns.
 #include "ffn_common.cuh"
+#include "ffn_few.h"
 #include "mhc_dispatch.h"
 #include "tc_pair.cuh"
 
 namespace mhc {
 
 namespace ftc {
-constexpr int TM = 256, TN = 256, TK = 64;  // the pair's tile, and the k block
-constexpr int HALF = 128;                   // rows of A and of B that one CTA brings
-constexpr int OPND = HALF * TK * 2;         // 16 KB
-constexpr int STAGE = 2 * OPND;
+constexpr int TM = 256, TK = 64;  // the pair's rows, and the k block
+constexpr int HALF = 128;         // rows of A that one CTA brings
+constexpr int ABYTES = HALF * TK * 2;
 constexpr int NS = 6;
-constexpr int OUT = 32 * 128;               // one staged output box: 32 rows of 128 bytes
-constexpr int NEPI = 4;                     // epilogue warps, two output boxes each
-constexpr int OUT_OFF = NS * STAGE;
-constexpr int BAR_OFF = OUT_OFF + NEPI * 2 * OUT;
-constexpr int SMEM = BAR_OFF + 256 + 1024;
+constexpr int NEPI = 4;           // epilogue warps
 constexpr int NT = 256;
 constexpr int BAND = 8;
-static_assert(SMEM <= 232448, "shared memory");
+constexpr int kChunk = 8;         // fp32: k blocks per stay in an accumulator
+constexpr int HBOX = 32 * 64;     // one staged box of results: 32 rows of 32 bf16 ...
+constexpr int FBOX = 32 * 128;    // ... or of 32 fp32
+
+template <int TN, bool F32> struct Cfg {
+  static constexpr int BROWS = TN / 2;                  // rows of B that one CTA brings
+  static constexpr int STAGE = ABYTES + BROWS * TK * 2;
+  static constexpr int OUT = F32 ? 16384 : 8192;        // staged results per epilogue warp
+  static constexpr int OUT_OFF = NS * STAGE;
+  static constexpr int BAR_OFF = OUT_OFF + NEPI * OUT;
+  static constexpr int SMEM = BAR_OFF + 256 + 1024;
+  static_assert(STAGE % 1024 == 0 && SMEM <= 232448, "shared memory");
+  static_assert((F32 ? 3 : 2) * TN <= 512, "TMEM columns");
+};
 }  // namespace ftc
 
 namespace {
@@ -85,115 +98,74 @@ __device__ __forceinline__ void tile_at(const GemmArgs& P, int64_t id, int& z, i
   mi = m0 + (int)(in % rows);
 }
 
-// One operand half of a stage: 128 rows x 64 k.  Stored along k: one box.
-// Stored along its rows (MN): two boxes of 64 rows.
-template <bool MN>
-__device__ __forceinline__ void load_half(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+// One operand of a stage: ROWS rows x 64 k.  Stored along k: one box.  Stored
+// along its rows (MN): boxes of 64 rows.
+template <int ROWS, bool MN>
+__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* map, uint32_t bar,
                                           int row0, int k0, int plane, uint64_t pol) {
   if (MN) {
-    tc::tma2_load_3d(dst, map, bar, row0, k0, plane, pol);
-    tc::tma2_load_3d(dst + ftc::OPND / 2, map, bar, row0 + 64, k0, plane, pol);
+#pragma unroll
+    for (int r = 0; r < ROWS; r += 64)
+      tc::tma2_load_3d(dst + r * 128, map, bar, row0 + r, k0, plane, pol);
   } else {
     tc::tma2_load_3d(dst, map, bar, k0, row0, plane, pol);
   }
 }
-// The descriptor of the k-th 16-wide slice of that half.
-template <bool MN> __device__ __forceinline__ uint64_t half_desc(uint32_t base, int k) {
-  return MN ? tc::smem_desc(base + k * 2048, ftc::OPND / 2, 1024, tc::SWZ_128B)
+// The descriptor of the k-th 16-wide slice of that operand.
+template <bool MN> __device__ __forceinline__ uint64_t rows_desc(uint32_t base, int k) {
+  return MN ? tc::smem_desc(base + k * 2048, 8192, 1024, tc::SWZ_128B)
             : tc::smem_desc(base + k * 32, 16, 1024, tc::SWZ_128B);
 }
-
-// An epilogue warp's output boxes: 32 rows of 128 bytes each, two in turn.
-struct Stager {
-  uint8_t* buf;
-  int n, lane;
-  __device__ __forceinline__ uint8_t* next() {
-    if (lane == 0) tc::bulk_wait_read<1>();
-    __syncwarp();
-    return buf + (n++ & 1) * ftc::OUT;
-  }
-  // piece p (16 bytes) of this lane's row
-  __device__ __forceinline__ void put(uint8_t* b, int p, uint4 v) {
-    *reinterpret_cast<uint4*>(b + lane * 128 + ((p ^ (lane & 7)) << 4)) = v;
-  }
-  __device__ __forceinline__ void send(uint8_t* b, const CUtensorMap* map, int64_t col,
-                                       int64_t row, int plane, bool inside) {
-    tc::fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-      if (inside) tc::tma_store_3d(map, tc::smem_u32(b), (int)col, (int)row, plane);
-      tc::bulk_commit();
-    }
-  }
-};
 
 __device__ __forceinline__ uint32_t bf2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// 32 values of this lane's row to columns [32 half, 32 half + 32) of a bf16 box.
-__device__ __forceinline__ void put_bf16(Stager& st, uint8_t* b, int half, const float (&v)[32]) {
+// Columns [16 g, 16 g + 16) of row `lane` of a staged box: 64-byte rows with the
+// 64-byte swizzle (bf16), 128-byte rows with the 128-byte swizzle (fp32).
+__device__ __forceinline__ void put_bf16(uint8_t* box, int lane, int g, const float (&v)[16]) {
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+    *reinterpret_cast<uint4*>(box + lane * 64 + (((2 * g + p) ^ ((lane >> 1) & 3)) << 4)) =
+        make_uint4(bf2(v[8 * p], v[8 * p + 1]), bf2(v[8 * p + 2], v[8 * p + 3]),
+                   bf2(v[8 * p + 4], v[8 * p + 5]), bf2(v[8 * p + 6], v[8 * p + 7]));
+}
+__device__ __forceinline__ void put_f32(uint8_t* box, int lane, int g, const float (&v)[16]) {
 #pragma unroll
   for (int p = 0; p < 4; ++p)
-    st.put(b, 4 * half + p,
-           make_uint4(bf2(v[8 * p], v[8 * p + 1]), bf2(v[8 * p + 2], v[8 * p + 3]),
-                      bf2(v[8 * p + 4], v[8 * p + 5]), bf2(v[8 * p + 6], v[8 * p + 7])));
+    *reinterpret_cast<float4*>(box + lane * 128 + (((4 * g + p) ^ (lane & 7)) << 4)) =
+        make_float4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
 }
-__device__ __forceinline__ void put_f32(Stager& st, uint8_t* b, const float (&v)[32]) {
-#pragma unroll
-  for (int p = 0; p < 8; ++p)
-    st.put(b, p, make_uint4(__float_as_uint(v[4 * p]), __float_as_uint(v[4 * p + 1]),
-                            __float_as_uint(v[4 * p + 2]), __float_as_uint(v[4 * p + 3])));
-}
-
-// A 64-column chunk of this warp's 32 rows.  bf16: one box.  fp32: the three
-// bf16 planes of the values (SPLIT; they are the next product's operand) or the
-// values themselves as two boxes.
-template <bool F32, bool SPLIT>
-__device__ __forceinline__ void emit(Stager& st, const CUtensorMap* map, int64_t col, int64_t row,
-                                     int plane, int64_t M, int64_t N, float (&v0)[32],
-                                     float (&v1)[32]) {
-  const bool in = row < M && col < N;
+// A value that the next product takes as an operand: itself in bf16, or its three
+// planes in three boxes.
+template <bool F32>
+__device__ __forceinline__ void put_operand(uint8_t* box, int lane, int g, const float (&v)[16]) {
   if (!F32) {
-    uint8_t* b = st.next();
-    put_bf16(st, b, 0, v0);
-    put_bf16(st, b, 1, v1);
-    st.send(b, map, col, row, plane, in);
-  } else if (SPLIT) {
-#pragma unroll 1
-    for (int pl = 0; pl < 3; ++pl) {
-      uint8_t* b = st.next();
-      float t0[32], t1[32];
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        float h, m, l;
-        split3(v0[i], h, m, l);
-        t0[i] = pl == 0 ? h : pl == 1 ? m : l;
-        split3(v1[i], h, m, l);
-        t1[i] = pl == 0 ? h : pl == 1 ? m : l;
-      }
-      put_bf16(st, b, 0, t0);
-      put_bf16(st, b, 1, t1);
-      st.send(b, map, col, row, 3 * plane + pl, in);
-    }
+    put_bf16(box, lane, g, v);
   } else {
-    uint8_t* b = st.next();
-    put_f32(st, b, v0);
-    st.send(b, map, col, row, plane, in);
-    b = st.next();
-    put_f32(st, b, v1);
-    st.send(b, map, col + 32, row, plane, row < M && col + 32 < N);
+    float h[16], m[16], l[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) split3(v[i], h[i], m[i], l[i]);
+    put_bf16(box, lane, g, h);
+    put_bf16(box + ftc::HBOX, lane, g, m);
+    put_bf16(box + 2 * ftc::HBOX, lane, g, l);
   }
 }
-
-// 32 columns of this lane's row of g or u; columns past the end are not read.
 template <bool F32>
-__device__ __forceinline__ void row32(const void* base, int64_t row, int64_t col, int64_t M,
-                                      int64_t N, float (&v)[32]) {
+__device__ __forceinline__ void put_value(uint8_t* box, int lane, int g, const float (&v)[16]) {
+  if (F32) put_f32(box, lane, g, v);
+  else put_bf16(box, lane, g, v);
+}
+
+// 16 columns of this lane's row of g or u, from column col on; what lies past the
+// end is not read.
+template <bool F32>
+__device__ __forceinline__ void row16(const void* base, int64_t row, int64_t col, int64_t M,
+                                      int64_t N, float (&v)[16]) {
   constexpr int VN = F32 ? 4 : 8;
 #pragma unroll
-  for (int i = 0; i < 32; i += VN) {
+  for (int i = 0; i < 16; i += VN) {
     if (row < M && col + i < N) {
       if (F32) {
         const float4 q = *reinterpret_cast<const float4*>((const float*)base + row * N + col + i);
@@ -211,15 +183,17 @@ __device__ __forceinline__ void row32(const void* base, int64_t row, int64_t col
   }
 }
 
-template <Epi E, bool AMN, bool BMN, bool F32>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ftc::NT, 1)
+template <Epi E, bool AMN, bool BMN, bool F32, int TN>
+__global__ void __launch_bounds__(ftc::NT, 1)
     k_ffn_tc(const __grid_constant__ GemmArgs P) {
   using namespace ftc;
+  using G = Cfg<TN, F32>;
+  constexpr int STAGE = G::STAGE, HN = TN / 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~(uintptr_t)1023);
   // full[NS] empty[NS] tfull[2] tempty[2] fin
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + BAR_OFF);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + G::BAR_OFF);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * NS + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   auto full = [&](int s) { return tc::smem_u32(bars + s); };
@@ -260,6 +234,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ftc::NT, 1)
   __syncthreads();
   tc::cluster_sync();  // the partner's barriers exist
   tc::tc_fence_after();
+  tc::grid_release();
+  tc::grid_wait();
   const uint32_t tmem = *tmem_slot;
 
   auto give_up = [&]() {
@@ -277,7 +253,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ftc::NT, 1)
         int z, mi, ni;
         tile_at(P, id, z, mi, ni);
         const int arow = mi * TM + rank * HALF;
-        const int brow = DUAL ? ni * HALF : ni * TN + rank * HALF;
+        const int brow = DUAL ? ni * HN : ni * TN + rank * HN;
         for (int sg = 0; sg < P.nseg && ok; ++sg) {
           const CUtensorMap* am = &P.a[P.am[sg]];
           const CUtensorMap* bm = &P.b[DUAL ? rank : P.bm[sg]];
@@ -293,8 +269,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ftc::NT, 1)
             const uint32_t base = tc::smem_u32(smem + s * STAGE);
             if (rank == 0) tc::mbar_arrive_expect_tx(full(s), 2 * STAGE);
             const uint32_t bar = tc::map_cta(full(s), 0);
-            load_half<AMN>(base, am, bar, arow, kb * TK, ap, pol);
-            load_half<BMN>(base + OPND, bm, bar, brow, kb * TK, bp, pol);
+            load_rows<HALF, AMN>(base, am, bar, arow, kb * TK, ap, pol);
+            load_rows<HN, BMN>(base + ABYTES, bm, bar, brow, kb * TK, bp, pol);
           }
         }
       }
@@ -317,35 +293,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ftc::NT, 1)
     // ---------------------------------------------------------------- MMA
     if (lane == 0 && rank == 0) {
       constexpr uint32_t idesc = tc::idesc_bf16(TM, TN, AMN, BMN);
+      const int nk = P.nseg * P.kblocks;
       int64_t it = 0;
-      int n = 0;
+      int n = 0;  // accumulators filled so far
       bool ok = true, any = false;
-      for (int64_t id = pair; id < tiles && ok; id += npairs, ++n) {
-        const int buf = n & 1;
-        if (n >= 2 && !tc::mbar_pipe_wait<true>(tempty(buf), ((uint32_t)(n / 2) & 1u) ^ 1u,
-                                                abort_flag, P.wait_ns)) {
-          give_up();
-          break;
-        }
-        tc::tc_fence_after();
-        for (int j = 0; j < P.nseg * P.kblocks; ++j, ++it) {
-          const int s = (int)(it % NS);
-          if (!tc::mbar_pipe_wait<false>(full(s), (uint32_t)(it / NS) & 1u, abort_flag,
-                                         P.wait_ns)) {
+      for (int64_t id = pair; id < tiles && ok; id += npairs) {
+        for (int j0 = 0; j0 < nk && ok; j0 += F32 ? kChunk : nk, ++n) {
+          const int j1 = F32 && j0 + kChunk < nk ? j0 + kChunk : nk;
+          const int buf = n & 1;
+          if (n >= 2 && !tc::mbar_pipe_wait<true>(tempty(buf), ((uint32_t)(n / 2) & 1u) ^ 1u,
+                                                  abort_flag, P.wait_ns)) {
             give_up();
             ok = false;
             break;
           }
           tc::tc_fence_after();
-          const uint32_t base = tc::smem_u32(smem + s * STAGE);
+          for (int j = j0; j < j1; ++j, ++it) {
+            const int s = (int)(it % NS);
+            if (!tc::mbar_pipe_wait<false>(full(s), (uint32_t)(it / NS) & 1u, abort_flag,
+                                           P.wait_ns)) {
+              give_up();
+              ok = false;
+              break;
+            }
+            tc::tc_fence_after();
+            const uint32_t base = tc::smem_u32(smem + s * STAGE);
 #pragma unroll
-          for (int k = 0; k < TK / 16; ++k)
-            tc::mma2_bf16(tmem + buf * TN, half_desc<AMN>(base, k), half_desc<BMN>(base + OPND, k),
-                          idesc, (j | k) != 0 ? 1u : 0u);
-          any = true;
-          tc::mma2_commit(empty(s));
+            for (int k = 0; k < TK / 16; ++k)
+              tc::mma2_bf16(tmem + buf * TN, rows_desc<AMN>(base, k),
+                            rows_desc<BMN>(base + ABYTES, k), idesc, j > j0 || k > 0 ? 1u : 0u);
+            any = true;
+            tc::mma2_commit(empty(s));
+          }
+          if (ok) tc::mma2_commit(tfull(buf));
         }
-        if (ok) tc::mma2_commit(tfull(buf));
       }
       // every MMA issued here has finished before TMEM is freed
       if (any) {
@@ -355,81 +336,137 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ftc::NT, 1)
     }
   } else if (warp >= 4) {
     // ----------------------------------------------------------- epilogue
-    const int q = warp & 3;  // TMEM lane quarter this warp may read
-    Stager st{smem + OUT_OFF + q * 2 * OUT, 0, lane};
+    // 32 columns at a time, staged as boxes of this warp's 32 rows and stored by
+    // TMA; SETS of boxes in turn.  The loops stay rolled: in a small problem the
+    // first pass over the code is a pass through instruction-cache misses.
+    constexpr int NB = F32 ? 3 : 1;  // boxes of one operand
+    constexpr int FB = F32 ? FBOX : HBOX;
+    constexpr int SET = E == EPI_STORE ? FB
+                        : E == EPI_GATE ? NB * HBOX
+                        : E == EPI_KEEP ? 2 * FB + NB * HBOX
+                                        : 2 * NB * HBOX;
+    constexpr int SETS = G::OUT / SET > 4 ? 4 : G::OUT / SET;
+    constexpr int STEP = SET % 1024 ? SET + 1024 - SET % 1024 : SET;
+    static_assert(SETS >= 1 && STEP * SETS <= G::OUT, "staged results");
+    constexpr int COLS = DUAL ? HN : TN;  // columns of D's tile
+    const int q = warp & 3;               // TMEM lane quarter this warp may read
+    uint8_t* out = smem + G::OUT_OFF + q * G::OUT;
+    const int nk = P.nseg * P.kblocks;
+    const int chunks = F32 ? (nk + kChunk - 1) / kChunk : 1;
+    const uint32_t master = tmem + ((uint32_t)(32 * q) << 16) + 2 * TN;
     // a tile's products may rightly take longer than one wait: 4 us per k block more
-    const uint64_t tile_ns = P.wait_ns + (uint64_t)P.nseg * P.kblocks * 4000;
-    int n = 0;
-    for (int64_t id = pair; id < tiles; id += npairs, ++n) {
+    const uint64_t tile_ns = P.wait_ns + (uint64_t)nk * 4000;
+    int n = 0, nset = 0;
+    for (int64_t id = pair; id < tiles; id += npairs) {
       int z, mi, ni;
       tile_at(P, id, z, mi, ni);
-      const int buf = n & 1;
-      bool ok = tc::mbar_pipe_wait<false>(tfull(buf), (uint32_t)(n / 2) & 1u, abort_flag, tile_ns);
-      if (!ok && !*abort_flag) give_up();
-      ok = __all_sync(0xffffffffu, ok);  // the TMEM loads below are warp-collective
-      if (!ok) break;
-      tc::tc_fence_after();
       const int64_t row0 = (int64_t)mi * TM + rank * HALF + 32 * q, row = row0 + lane;
-      const uint32_t ta = tmem + ((uint32_t)(32 * q) << 16) + buf * TN;
-      if (DUAL) {
+      bool ok = true;
+      for (int ch = 0; ch < chunks; ++ch, ++n) {
+        const int buf = n & 1;
+        ok = tc::mbar_pipe_wait<false>(tfull(buf), (uint32_t)(n / 2) & 1u, abort_flag, tile_ns);
+        if (!ok && !*abort_flag) give_up();
+        ok = __all_sync(0xffffffffu, ok);  // the TMEM loads below are warp-collective
+        if (!ok) break;
+        tc::tc_fence_after();
+        const uint32_t ta = tmem + ((uint32_t)(32 * q) << 16) + buf * TN;
+        if (F32 && ch + 1 < chunks) {
+          // not the last stay: add it to the sums so far
 #pragma unroll 1
-        for (int c = 0; c < HALF; c += 64) {
-          const int64_t col = (int64_t)ni * HALF + c;
-          if (E == EPI_GATE) {
-            float v[2][32];
+          for (int c = 0; c < TN; c += 16) {
+            float v[16], m[16];
+            if (ch == 0) {
+              tc::tmem_get16(ta + c, v);
+            } else {
+              tc::tmem_get16x2(ta + c, master + c, v, m);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float u[32];
-              tc::tmem_get32x2(ta + c + 32 * h, ta + HALF + c + 32 * h, v[h], u);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[h][i] = gate<!F32>(P.act, v[h][i]) * u[i];
+              for (int i = 0; i < 16; ++i) v[i] += m[i];
             }
-            emit<F32, true>(st, &P.d[0], col, row0, 0, P.M, P.N, v[0], v[1]);
-          } else {
-            float g[2][32], u[2][32];
-            tc::tmem_get32x2(ta + c, ta + c + 32, g[0], g[1]);
-            emit<F32, false>(st, &P.d[1], col, row0, 0, P.M, P.N, g[0], g[1]);
-            tc::tmem_get32x2(ta + HALF + c, ta + HALF + c + 32, u[0], u[1]);
-            emit<F32, false>(st, &P.d[2], col, row0, 0, P.M, P.N, u[0], u[1]);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int i = 0; i < 32; ++i) g[h][i] = gate<!F32>(P.act, g[h][i]) * u[h][i];
-            emit<F32, true>(st, &P.d[0], col, row0, 0, P.M, P.N, g[0], g[1]);
+            tc::tmem_put16(master + c, v);
           }
-        }
-      } else {
+        } else {
+          // D's columns [c, c + 16)
+          auto sums = [&](int c, float (&v)[16]) {
+            if (F32 && chunks > 1) {
+              float m[16];
+              tc::tmem_get16x2(ta + c, master + c, v, m);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] += m[i];
+            } else {
+              tc::tmem_get16(ta + c, v);
+            }
+          };
 #pragma unroll 1
-        for (int c = 0; c < TN; c += 64) {
-          const int64_t col = (int64_t)ni * TN + c;
-          if (E == EPI_STORE) {
-            float v[2][32];
-            tc::tmem_get32x2(ta + c, ta + c + 32, v[0], v[1]);
-            emit<F32, false>(st, &P.d[z], col, row0, 0, P.M, P.N, v[0], v[1]);
-          } else {
-            float dg[2][32], du[2][32];
+          for (int c = 0; c < COLS; c += 32) {
+            const int64_t col = (int64_t)ni * COLS + c;
+            const bool in = row0 < P.M && col < P.N;
+            uint8_t* box = out + (nset++ % SETS) * STEP;
+            if (lane == 0) tc::bulk_wait_read<SETS - 1>();
+            __syncwarp();
+#pragma unroll 1
+            for (int g = 0; g < 2; ++g) {
+              const int cg = c + 16 * g;
+              float v[16];
+              if (E == EPI_STORE) {
+                sums(cg, v);
+                put_value<F32>(box, lane, g, v);
+              } else if (DUAL) {
+                float u[16];
+                sums(cg, v);
+                sums(HN + cg, u);
+                if (E == EPI_KEEP) {
+                  put_value<F32>(box, lane, g, v);
+                  put_value<F32>(box + FB, lane, g, u);
+                }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float u[32], da[32];
-              row32<F32>(P.g, row, col + 32 * h, P.M, P.N, dg[h]);
-              row32<F32>(P.u, row, col + 32 * h, P.M, P.N, u);
-              tc::tmem_get32(ta + c + 32 * h, da);
+                for (int i = 0; i < 16; ++i) v[i] = gate<!F32>(P.act, v[i]) * u[i];
+                put_operand<F32>(box + (E == EPI_KEEP ? 2 * FB : 0), lane, g, v);
+              } else {
+                float u[16], gv[16];
+                row16<F32>(P.g, row, col + 16 * g, P.M, P.N, gv);
+                row16<F32>(P.u, row, col + 16 * g, P.M, P.N, u);
+                sums(cg, v);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                float a, da_dg;
-                gate_both<!F32>(P.act, dg[h][i], a, da_dg);
-                dg[h][i] = da[i] * u[i] * da_dg;
-                du[h][i] = da[i] * a;
+                for (int i = 0; i < 16; ++i) {
+                  float h, dh;
+                  gate_both<!F32>(P.act, gv[i], h, dh);
+                  u[i] = v[i] * u[i] * dh;
+                  v[i] *= h;
+                }
+                put_operand<F32>(box, lane, g, u);
+                put_operand<F32>(box + NB * HBOX, lane, g, v);
               }
             }
-            emit<F32, true>(st, &P.d[0], col, row0, 0, P.M, P.N, dg[0], dg[1]);
-            emit<F32, true>(st, &P.d[0], col, row0, 1, P.M, P.N, du[0], du[1]);
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (in) {
+                const uint32_t b = tc::smem_u32(box);
+                const int cc = (int)col, rr = (int)row0;
+                if (E == EPI_STORE) {
+                  tc::tma_store_3d(&P.d[z], b, cc, rr, 0);
+                } else if (E == EPI_DGATE) {
+                  for (int pl = 0; pl < 2 * NB; ++pl)
+                    tc::tma_store_3d(&P.d[0], b + pl * HBOX, cc, rr, pl);
+                } else {
+                  if (E == EPI_KEEP) {
+                    tc::tma_store_3d(&P.d[1], b, cc, rr, 0);
+                    tc::tma_store_3d(&P.d[2], b + FB, cc, rr, 0);
+                  }
+                  for (int pl = 0; pl < NB; ++pl)
+                    tc::tma_store_3d(&P.d[0], b + (E == EPI_KEEP ? 2 * FB : 0) + pl * HBOX, cc, rr,
+                                     pl);
+                }
+              }
+              tc::bulk_commit();
+            }
           }
         }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive_cluster(tc::map_cta(tempty(buf), 0));
       }
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive_cluster(tc::map_cta(tempty(buf), 0));
+      if (!ok) break;
     }
     if (lane == 0) tc::bulk_wait<0>();
   }
@@ -478,11 +515,12 @@ struct Mat {
   bool f32;
 };
 
-// mn: the operand's own rows run along the stored columns.
-cudaError_t operand_map(CUtensorMap* m, const Mat& x, bool mn) {
+// mn: the operand's own rows run along the stored columns; otherwise boxes of
+// `rows` rows.
+cudaError_t operand_map(CUtensorMap* m, const Mat& x, bool mn, int rows) {
   const uint64_t d[3] = {(uint64_t)x.cols, (uint64_t)x.rows, (uint64_t)x.planes};
   const uint64_t s[2] = {(uint64_t)x.cols * 2, (uint64_t)x.cols * x.rows * 2};
-  const uint32_t b[3] = {64, mn ? 64u : (uint32_t)ftc::HALF, 1};
+  const uint32_t b[3] = {64, mn ? 64u : (uint32_t)rows, 1};
   return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x.p, 3, d, s, b,
                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
@@ -490,9 +528,10 @@ cudaError_t result_map(CUtensorMap* m, const Mat& x) {
   const uint64_t e = x.f32 ? 4 : 2;
   const uint64_t d[3] = {(uint64_t)x.cols, (uint64_t)x.rows, (uint64_t)x.planes};
   const uint64_t s[2] = {(uint64_t)x.cols * e, (uint64_t)x.cols * x.rows * e};
-  const uint32_t b[3] = {(uint32_t)(128 / e), 32, 1};
+  const uint32_t b[3] = {32, 32, 1};
   return make_tmap(m, x.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                   x.p, 3, d, s, b, CU_TENSOR_MAP_SWIZZLE_128B,
+                   x.p, 3, d, s, b,
+                   x.f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                    CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 
@@ -512,21 +551,63 @@ void segments(GemmArgs& P, int pairs, int np) {
       }
 }
 
-template <Epi E, bool AMN, bool BMN, bool F32> cudaError_t launch(GemmArgs& P, cudaStream_t s) {
-  auto kern = k_ffn_tc<E, AMN, BMN, F32>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ftc::SMEM);
-  if (e != cudaSuccess) return e;
+int sm_pairs() {
   int dev = 0, sms = 148;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     sms = 148;
-  const int64_t tiles = (int64_t)P.mt * P.nt * P.nz, pairs = sms / 2;
-  kern<<<(unsigned)(2 * (tiles < pairs ? tiles : pairs)), ftc::NT, ftc::SMEM, s>>>(P);
-  return cudaGetLastError();
+  return sms / 2;
 }
 
 int tiles_of(int64_t n, int t) { return (int)((n + t - 1) / t); }
+
+#define TRY(call)                         \
+  do {                                    \
+    const cudaError_t e_ = (call);        \
+    if (e_ != cudaSuccess) return e_;     \
+  } while (0)
+
+// The operands of a launch as stored, with the length of the sums.
+struct Opnds {
+  Mat a, b[2];
+  int64_t K;
+};
+
+template <Epi E, bool AMN, bool BMN, bool F32, int TN>
+cudaError_t launch_tn(GemmArgs& P, const Opnds& o, cudaStream_t s) {
+  constexpr bool DUAL = E == EPI_GATE || E == EPI_KEEP;
+  using G = ftc::Cfg<TN, F32>;
+  TRY(operand_map(&P.a[0], o.a, AMN, ftc::HALF));
+  TRY(operand_map(&P.b[0], o.b[0], BMN, G::BROWS));
+  if (o.b[1].p) TRY(operand_map(&P.b[1], o.b[1], BMN, G::BROWS));
+  P.kblocks = tiles_of(o.K, ftc::TK);
+  P.mt = tiles_of(P.M, ftc::TM);
+  P.nt = tiles_of(P.N, DUAL ? TN / 2 : TN);
+  auto kern = k_ffn_tc<E, AMN, BMN, F32, TN>;
+  TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM));
+  const int64_t tiles = (int64_t)P.mt * P.nt * P.nz, pairs = sm_pairs();
+  return launch_after(kern, (unsigned)(2 * (tiles < pairs ? tiles : pairs)), ftc::NT, G::SMEM, 2, s,
+                      P);
+}
+
+// fp32: 256 x 128 tiles (three TMEM regions).  bf16: 256 x 256, or 256 x 128
+// where its rounds over the pairs come to less: a narrow tile has half the work
+// and takes 0.72 of the time (T = 8192, C = 7168, F = 14336: 5.41 against 3.63 ms
+// for the forward pass).
+template <Epi E, bool AMN, bool BMN, bool F32>
+cudaError_t launch(GemmArgs& P, const Opnds& o, cudaStream_t s) {
+  if constexpr (F32) {
+    return launch_tn<E, AMN, BMN, true, 128>(P, o, s);
+  } else {
+    constexpr bool DUAL = E == EPI_GATE || E == EPI_KEEP;
+    const int64_t rows = (int64_t)tiles_of(P.M, ftc::TM) * P.nz, pairs = sm_pairs();
+    const int64_t wide = rows * tiles_of(P.N, DUAL ? 128 : 256);
+    const int64_t half = rows * tiles_of(P.N, DUAL ? 64 : 128);
+    if (72 * ((half + pairs - 1) / pairs) < 100 * ((wide + pairs - 1) / pairs))
+      return launch_tn<E, AMN, BMN, false, 128>(P, o, s);
+    return launch_tn<E, AMN, BMN, false, 256>(P, o, s);
+  }
+}
 
 // Operands as the products take them: the caller's bf16 arrays, or the split
 // copies of its fp32 arrays.
@@ -536,64 +617,45 @@ struct Ffn {
   const void *x, *wg, *wu, *wd, *gy;
   int* st;
   int64_t wait_ns;
+  FewArgs few() const { return {t, C, F, act, x, wg, wu, wd, gy, st, wait_ns}; }
 };
 
-GemmArgs base_args(const Ffn& f) {
+// A launch of `pairs` products into an M x N result.
+GemmArgs base_args(const Ffn& f, int pairs, int64_t M, int64_t N) {
   GemmArgs P{};
   P.nz = 1;
+  P.M = M;
+  P.N = N;
   P.act = f.act;
   P.status = f.st;
   P.wait_ns = tc::wait_limit(f.wait_ns);
+  segments(P, pairs, f.np);
   return P;
 }
-
-#define TRY(call)                         \
-  do {                                    \
-    const cudaError_t e_ = (call);        \
-    if (e_ != cudaSuccess) return e_;     \
-  } while (0)
 
 // a = act(x wg^T) * (x wu^T) to a (and g, u where they are kept)
 template <bool F32> cudaError_t gate_product(const Ffn& f, void* a, void* g, void* u,
                                              cudaStream_t s) {
-  GemmArgs P = base_args(f);
-  TRY(operand_map(&P.a[0], {f.x, f.t, f.C, f.np, false}, false));
-  TRY(operand_map(&P.b[0], {f.wg, f.F, f.C, f.np, false}, false));
-  TRY(operand_map(&P.b[1], {f.wu, f.F, f.C, f.np, false}, false));
+  GemmArgs P = base_args(f, 1, f.t, f.F);
+  const Opnds o{{f.x, f.t, f.C, f.np, false},
+                {{f.wg, f.F, f.C, f.np, false}, {f.wu, f.F, f.C, f.np, false}}, f.C};
   TRY(result_map(&P.d[0], {a, f.t, f.F, f.np, false}));
-  segments(P, 1, f.np);
-  P.kblocks = tiles_of(f.C, ftc::TK);
-  P.mt = tiles_of(f.t, ftc::TM);
-  P.nt = tiles_of(f.F, ftc::HALF);
-  P.M = f.t;
-  P.N = f.F;
-  if (g == nullptr) return launch<EPI_GATE, false, false, F32>(P, s);
+  if (g == nullptr) return launch<EPI_GATE, false, false, F32>(P, o, s);
   TRY(result_map(&P.d[1], {g, f.t, f.F, 1, F32}));
   TRY(result_map(&P.d[2], {u, f.t, f.F, 1, F32}));
-  return launch<EPI_KEEP, false, false, F32>(P, s);
-}
-
-// D (rows x cols) = A B^T over K; A, B given as stored
-template <Epi E, bool AMN, bool BMN, bool F32>
-cudaError_t product(GemmArgs& P, const Ffn& f, const Mat& A, const Mat& B, int64_t K, int64_t M,
-                    int64_t N, cudaStream_t s) {
-  TRY(operand_map(&P.a[0], A, AMN));
-  TRY(operand_map(&P.b[0], B, BMN));
-  P.kblocks = tiles_of(K, ftc::TK);
-  P.mt = tiles_of(M, ftc::TM);
-  P.nt = tiles_of(N, ftc::TN);
-  P.M = M;
-  P.N = N;
-  return launch<E, AMN, BMN, F32>(P, s);
+  return launch<EPI_KEEP, false, false, F32>(P, o, s);
 }
 
 template <bool F32> cudaError_t fwd(const Ffn& f, void* y, void* a, cudaStream_t s) {
+  if (!F32 && f.t <= kFewTokens) {
+    TRY(few_gate(f.few(), a, nullptr, nullptr, s));
+    return few_down(f.few(), a, y, s);
+  }
   TRY(gate_product<F32>(f, a, nullptr, nullptr, s));
-  GemmArgs P = base_args(f);
-  segments(P, 1, f.np);
+  GemmArgs P = base_args(f, 1, f.t, f.C);
   TRY(result_map(&P.d[0], {y, f.t, f.C, 1, F32}));
-  return product<EPI_STORE, false, false, F32>(P, f, {a, f.t, f.F, f.np, false},
-                                               {f.wd, f.C, f.F, f.np, false}, f.F, f.t, f.C, s);
+  return launch<EPI_STORE, false, false, F32>(
+      P, {{a, f.t, f.F, f.np, false}, {{f.wd, f.C, f.F, f.np, false}}, f.F}, s);
 }
 
 // a [np][t][F], d [2 np][t][F] (dg, du), g and u [t][F] in the call's type.  For
@@ -603,39 +665,39 @@ template <bool F32>
 cudaError_t bwd(const Ffn& f, void* gx, void* gwg, void* gwu, void* gwd, void* a, void* d, void* g,
                 void* u, cudaStream_t s) {
   const int np = f.np;
-  TRY(gate_product<F32>(f, a, g, u, s));
-  {
-    GemmArgs P = base_args(f);
-    segments(P, 1, np);
-    TRY(result_map(&P.d[0], {d, f.t, f.F, 2 * np, false}));
+  const Mat X{f.x, f.t, f.C, np, false}, GY{f.gy, f.t, f.C, np, false};
+  const Mat A{a, f.t, f.F, np, false}, D{d, f.t, f.F, 2 * np, false};
+  const Mat WG{f.wg, f.F, f.C, np, false}, WU{f.wu, f.F, f.C, np, false};
+  const Mat WD{f.wd, f.C, f.F, np, false};
+  const bool few = !F32 && f.t <= kFewTokens;
+  if (few) {
+    TRY(few_gate(f.few(), a, g, u, s));
+    TRY(few_dgate(f.few(), g, u, d, s));
+  } else {
+    TRY(gate_product<F32>(f, a, g, u, s));
+    GemmArgs P = base_args(f, 1, f.t, f.F);
+    TRY(result_map(&P.d[0], D));
     P.g = g;
     P.u = u;
-    TRY((product<EPI_DGATE, false, true, F32>(P, f, {f.gy, f.t, f.C, np, false},
-                                              {f.wd, f.C, f.F, np, false}, f.C, f.t, f.F, s)));
+    TRY((launch<EPI_DGATE, false, true, F32>(P, {GY, {WD}, f.C}, s)));
   }
   {
-    GemmArgs P = base_args(f);
-    segments(P, 1, np);
+    GemmArgs P = base_args(f, 1, f.C, f.F);
     TRY(result_map(&P.d[0], {gwd, f.C, f.F, 1, F32}));
-    TRY((product<EPI_STORE, true, true, F32>(P, f, {f.gy, f.t, f.C, np, false},
-                                             {a, f.t, f.F, np, false}, f.t, f.C, f.F, s)));
+    TRY((launch<EPI_STORE, true, true, F32>(P, {GY, {A}, f.t}, s)));
   }
   {
-    GemmArgs P = base_args(f);
-    segments(P, 1, np);
+    GemmArgs P = base_args(f, 1, f.F, f.C);
     P.nz = 2;
     P.zplanes = np;
     TRY(result_map(&P.d[0], {gwg, f.F, f.C, 1, F32}));
     TRY(result_map(&P.d[1], {gwu, f.F, f.C, 1, F32}));
-    TRY((product<EPI_STORE, true, true, F32>(P, f, {d, f.t, f.F, 2 * np, false},
-                                             {f.x, f.t, f.C, np, false}, f.t, f.F, f.C, s)));
+    TRY((launch<EPI_STORE, true, true, F32>(P, {D, {X}, f.t}, s)));
   }
-  GemmArgs P = base_args(f);
-  segments(P, 2, np);
+  if (few) return few_grad_x(f.few(), d, gx, s);
+  GemmArgs P = base_args(f, 2, f.t, f.C);
   TRY(result_map(&P.d[0], {gx, f.t, f.C, 1, F32}));
-  TRY(operand_map(&P.b[1], {f.wu, f.F, f.C, np, false}, true));
-  return product<EPI_STORE, false, true, F32>(P, f, {d, f.t, f.F, 2 * np, false},
-                                              {f.wg, f.F, f.C, np, false}, f.F, f.t, f.C, s);
+  return launch<EPI_STORE, false, true, F32>(P, {D, {WG, WU}, f.F}, s);
 }
 
 size_t up(size_t v) { return (v + 255) / 256 * 256; }
