@@ -80,59 +80,45 @@ __device__ __forceinline__ void load_param(const float* p, uint64_t (&v)[P]) {
   }
 }
 
-// What one warp knows of its share of a row: how many channels, their mean, the
-// squares about that mean and, in the backward, the sums of a and of a (x - m).
+// What one warp knows of its share of a row: the mean of its channels, the squares
+// about that mean and, in the backward, the sums of a and of a (x - m).
 struct Share {
-  float n, m, m2, a, ax;
+  float m, m2, a, ax;
 };
-
-// The row's statistics from its warps' shares (all lanes of all warps get them).
-// Record w is read by lane w, so at most 32 warps.
-template <bool BWD>
-__device__ __forceinline__ Share join_shares(const Share& mine, Share* rec, int nwarps, int64_t C) {
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (lane == 0) rec[warp] = mine;
-  __syncthreads();
-  Share q = lane < nwarps ? rec[lane] : Share{0.f, 0.f, 0.f, 0.f, 0.f};
-  Share r;
-  r.n = (float)C;
-  r.m = warp_sum(q.n * q.m) / (float)C;
-  const float d = q.m - r.m;
-  r.m2 = warp_sum(q.m2 + q.n * d * d);
-  r.a = r.ax = 0.f;
-  if (BWD) {
-    r.a = warp_sum(q.a);
-    r.ax = warp_sum(q.ax + d * q.a);
-  }
-  return r;
-}
 
 __device__ __forceinline__ void report(float mean, float s, int* status) {
   if (!isfinite(mean) || !isfinite(s)) flag_status(status, MHC_ERR_NONFINITE);
 }
 
-// Channels of the vectors k = first + lane, first + lane + stride, ... below
-// nvec that a warp's lanes hold, VPT per lane.
-__device__ __forceinline__ int share_channels(int vpt, int n, int first, int stride, int nvec) {
+// Channels that warp `warp` of a row of nvec vectors holds: vectors 32 warp + lane,
+// and every `stride` vectors after that.
+__device__ __forceinline__ float share_channels(int warp, int stride, int n, int nvec) {
   int c = 0;
-  for (int i = 0; i < vpt; ++i) {
-    const int left = nvec - first - i * stride;
-    c += left <= 0 ? 0 : left < 32 ? left : 32;
-  }
-  return c * n;
+  for (int k = 32 * warp; k < nvec; k += stride) c += nvec - k < 32 ? nvec - k : 32;
+  return (float)(c * n);
+}
+__device__ __forceinline__ float inv_or_0(float n) { return n > 0.f ? 1.0f / n : 0.f; }
+
+__device__ __forceinline__ void cp16(uint4* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // ------------------------------------------------------------------ forward
 // WARP: one row per warp (blockDim.x / 32 rows per CTA); otherwise one row per
 // CTA.  A thread holds VPT 16-byte vectors of its row.
-template <typename T, int VPT, bool WARP>
-__global__ void __launch_bounds__(WARP ? 128 : 512)
+template <typename T, int VPT, bool WARP, int MAXT>
+__global__ void __launch_bounds__(MAXT)
     k_norm_fwd(int64_t rows, int64_t C, float eps, const T* __restrict__ x,
                const float* __restrict__ w, const float* __restrict__ b, T* __restrict__ y,
                int* status) {
   constexpr int N = Vec<T>::N, P = Pairs<T>::P;
   using PV = Pairs<T>;
-  __shared__ Share rec[32];
+  __shared__ float3 rec[16];
   const int tpr = WARP ? 32 : blockDim.x;
   const int t = WARP ? threadIdx.x % 32 : threadIdx.x;
   const int64_t row = WARP ? (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32
@@ -141,36 +127,46 @@ __global__ void __launch_bounds__(WARP ? 128 : 512)
   if (WARP && row >= rows) return;
   const int nvec = (int)(C / N);
   const uint4* xr = reinterpret_cast<const uint4*>(x + row * C);
-  uint4 v[VPT];
-  uint64_t sum = 0;
+  uint4 raw[VPT];
+  uint64_t v[VPT][P], sum = 0;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int k = t + i * tpr;
-    v[i] = k < nvec ? __ldcs(xr + k) : make_uint4(0, 0, 0, 0);
+    raw[i] = k < nvec ? __ldcs(xr + k) : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
-    for (int e = 0; e < P; ++e) sum = f2add(sum, PV::get(v[i], e));
-  Share sh;
-  sh.n = WARP ? (float)C : (float)share_channels(VPT, N, t & ~31, tpr, nvec);
-  sh.m = sh.n > 0.f ? warp_sum(f2sum(sum)) / sh.n : 0.f;
-  uint64_t m2 = 0, nm = f2dup(-sh.m);
+    for (int e = 0; e < P; ++e) {
+      v[i][e] = PV::get(raw[i], e);
+      sum = f2add(sum, v[i][e]);
+    }
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const float n = WARP ? (float)C : share_channels(warp, tpr, N, nvec);
+  float m = warp_sum(f2sum(sum)) * inv_or_0(n);
+  uint64_t m2 = 0, nm = f2dup(-m);
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
     if (t + i * tpr < nvec) {
 #pragma unroll
       for (int e = 0; e < P; ++e) {
-        const uint64_t d = f2add(PV::get(v[i], e), nm);
+        const uint64_t d = f2add(v[i][e], nm);
         m2 = f2fma(d, d, m2);
       }
     }
-  sh.m2 = warp_sum(f2sum(m2));
-  if (!WARP) sh = join_shares<false>(sh, rec, blockDim.x / 32, C);
-  const float s = 1.0f / sqrtf(sh.m2 / (float)C + eps);
-  if (t == 0) report(sh.m, s, status);
-  nm = f2dup(-sh.m);
-  const uint64_t ss = f2dup(s);
+  float var = warp_sum(f2sum(m2));
+  const float inv_c = 1.0f / (float)C;
+  if (!WARP) {
+    if (lane == 0) rec[warp] = make_float3(n, m, var);
+    __syncthreads();
+    const float3 q = lane < tpr / 32 ? rec[lane] : make_float3(0.f, 0.f, 0.f);
+    m = warp_sum(q.x * q.y) * inv_c;
+    const float d = q.y - m;
+    var = warp_sum(q.z + q.x * d * d);
+  }
+  const float s = rsqrtf(var * inv_c + eps);
+  if (t == 0) report(m, s, status);
+  const uint64_t ss = f2dup(s), nms = f2dup(-m * s);
   uint4* yr = reinterpret_cast<uint4*>(y + row * C);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
@@ -181,10 +177,30 @@ __global__ void __launch_bounds__(WARP ? 128 : 512)
       if (b) load_param<P>(b + (int64_t)k * N, bv);
 #pragma unroll
       for (int e = 0; e < P; ++e)
-        o[e] = f2fma(f2mul(f2add(PV::get(v[i], e), nm), ss), wv[e], bv[e]);
+        o[e] = f2fma(f2fma(v[i][e], ss, nms), wv[e], bv[e]);
       __stcs(yr + k, PV::pack(o));
     }
   }
+}
+
+// A row's statistics from its warps' shares, for CTAs of kMaxThreads.
+__device__ __forceinline__ Share join_shares(float n, const Share& mine, float4* rec, float* cnt,
+                                             int64_t C) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (lane == 0) {
+    rec[warp] = make_float4(mine.m, mine.m2, mine.a, mine.ax);
+    cnt[warp] = n;
+  }
+  __syncthreads();
+  const float4 q = rec[lane];
+  const float nq = cnt[lane];
+  Share r;
+  r.m = warp_sum(nq * q.x) / (float)C;
+  const float d = q.x - r.m;
+  r.m2 = warp_sum(q.y + nq * d * d);
+  r.a = warp_sum(q.z);
+  r.ax = warp_sum(q.w + d * q.z);
+  return r;
 }
 
 // Rows too long for registers: one CTA per row, three walks over the row.
@@ -193,7 +209,8 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_fwd_long(
     int64_t C, float eps, const T* __restrict__ x, const float* __restrict__ w,
     const float* __restrict__ b, T* __restrict__ y, int* status) {
   constexpr int N = Vec<T>::N;
-  __shared__ Share rec[32];
+  __shared__ float4 rec[32];
+  __shared__ float num[32];
   const int64_t row = blockIdx.x, nvec = C / N;
   const T* xr = x + row * C;
   float sum = 0.f, v[N];
@@ -206,9 +223,9 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_fwd_long(
     sum += q;
     cnt += N;
   }
-  Share sh;
-  sh.n = warp_sum((float)cnt);
-  sh.m = sh.n > 0.f ? warp_sum(sum) / sh.n : 0.f;
+  Share sh = {};
+  const float n = warp_sum((float)cnt);
+  sh.m = warp_sum(sum) * inv_or_0(n);
   float m2 = 0.f;
   for (int64_t k = threadIdx.x; k < nvec; k += blockDim.x) {
     Vec<T>::load(xr + k * N, v);
@@ -218,8 +235,8 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_fwd_long(
     m2 += q;
   }
   sh.m2 = warp_sum(m2);
-  sh = join_shares<false>(sh, rec, blockDim.x / 32, C);
-  const float s = 1.0f / sqrtf(sh.m2 / (float)C + eps);
+  sh = join_shares(n, sh, rec, num, C);
+  const float s = rsqrtf(sh.m2 / (float)C + eps);
   if (threadIdx.x == 0) report(sh.m, s, status);
   for (int64_t k = threadIdx.x; k < nvec; k += blockDim.x) {
     Vec<T>::load(xr + k * N, v);
@@ -232,124 +249,174 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_fwd_long(
 }
 
 // ----------------------------------------------------------------- backward
-// Persistent CTAs: each takes rows in a fixed stride and keeps its threads'
-// channels of grad_weight and grad_bias in registers; one partial row pair
-// [2][C] per CTA, summed in CTA order by k_norm_fin.  x and grad_y come through
-// a ring of SLOTS rows in shared memory (cp.async: a thread copies what it later
-// reads itself, so no barrier is needed), the next rows on their way while one is
-// worked on.  WARP: one row per warp at a time, the warps' sums joined in warp
-// order through the ring's memory.
-__device__ __forceinline__ void cp16(uint4* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(dst)), "l"(src)
-               : "memory");
+// Persistent CTAs: each takes pairs of rows in a fixed stride and keeps its
+// threads' channels of grad_weight and grad_bias in registers; one partial row
+// pair [2][C] per CTA, summed in CTA order by k_norm_fin.  Two rows at a time
+// share the loads of the weight and half the shuffles (one half-warp reduces
+// each) and fill one row's waits with the other's work.  x and grad_y come
+// through a ring of two row pairs in shared memory (cp.async: a thread copies
+// what it later reads itself, so no barrier is needed).  WARP: a pair of rows per
+// warp, the warps' sums joined in warp order through the ring's memory.
+
+// Sums over the warp of a (row 0) and b (row 1): lanes 0..15 get row 0's, lanes
+// 16..31 row 1's.
+__device__ __forceinline__ float pair_sum(float a, float b, int lane) {
+  const bool hi = lane >= 16;
+  float v = (hi ? b : a) + __shfl_xor_sync(0xffffffffu, hi ? a : b, 16);
+#pragma unroll
+  for (int o = 8; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float half_sum(float v) {
+#pragma unroll
+  for (int o = 8; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
 }
 
-template <typename T, int VPT, bool WARP, int SLOTS, int MAXT, int PERSM>
+template <typename T, int VPT, bool WARP, int MAXT, int PERSM>
 __global__ void __launch_bounds__(MAXT, PERSM)
     k_norm_bwd(int64_t rows, int64_t C, float eps, const T* __restrict__ x,
                const float* __restrict__ w, const T* __restrict__ gy, T* __restrict__ gx,
                float* __restrict__ part, int* status) {
   constexpr int N = Vec<T>::N, P = Pairs<T>::P;
   using PV = Pairs<T>;
-  __shared__ Share rec[2][32];
-  extern __shared__ uint4 ring[];  // [group][SLOTS][x, gy][nvec]; WARP, at the end: [2][C] sums
+  __shared__ float4 rec[WARP ? 1 : 2][2][16];
+  extern __shared__ uint4 ring[];  // [group][2][row][x, gy][nvec]; WARP, at the end: [2][C]
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int tpr = WARP ? 32 : blockDim.x;
-  const int t = WARP ? threadIdx.x % 32 : threadIdx.x;
-  const int per = WARP ? blockDim.x / 32 : 1, g = WARP ? threadIdx.x / 32 : 0;
+  const int t = WARP ? lane : threadIdx.x;
+  const int per = WARP ? blockDim.x / 32 : 1, g = WARP ? warp : 0;
   const int nvec = (int)(C / N);
-  uint4* mine = ring + (int64_t)g * SLOTS * 2 * nvec;
-  const int64_t row0 = (int64_t)blockIdx.x * per + g, step = (int64_t)gridDim.x * per;
+  uint4* mine = ring + (int64_t)g * 8 * nvec;
+  const int64_t row0 = 2 * ((int64_t)blockIdx.x * per + g), step = 2 * (int64_t)gridDim.x * per;
+  const float inv_c = 1.0f / (float)C;
+  // this warp's channels, and those of the warp whose record this lane joins
+  const float inv_n = WARP ? inv_c : inv_or_0(share_channels(warp, tpr, N, nvec));
+  const float nq =
+      WARP || (lane & 15) >= tpr / 32 ? 0.f : share_channels(lane & 15, tpr, N, nvec);
   tc::grid_release();
   tc::grid_wait();
   auto fetch = [&](int64_t row, int slot) {
-    if (row < rows) {
-      uint4* d = mine + slot * 2 * nvec;
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int k = t + i * tpr;
-        if (k < nvec) {
-          cp16(d + k, x + row * C + (int64_t)k * N);
-          cp16(d + nvec + k, gy + row * C + (int64_t)k * N);
+    for (int r = 0; r < 2; ++r) {
+      if (row + r < rows) {
+        uint4* d = mine + (slot * 4 + 2 * r) * nvec;
+        const uint4* xr = reinterpret_cast<const uint4*>(x + (row + r) * C);
+        const uint4* gr = reinterpret_cast<const uint4*>(gy + (row + r) * C);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+          const int k = t + i * tpr;
+          if (k < nvec) {
+            cp16(d + k, xr + k);
+            cp16(d + nvec + k, gr + k);
+          }
         }
       }
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    cp_commit();
   };
   uint64_t gw[VPT][P], gb[VPT][P];
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
     for (int e = 0; e < P; ++e) gw[i][e] = gb[i][e] = 0;
-  const float share = WARP ? (float)C : (float)share_channels(VPT, N, t & ~31, tpr, nvec);
-#pragma unroll
-  for (int q = 0; q + 1 < SLOTS; ++q) fetch(row0 + q * step, q);
+  fetch(row0, 0);
   int it = 0;
   for (int64_t row = row0; row < rows; row += step, ++it) {
-    if (SLOTS == 1) fetch(row, 0);
-    else fetch(row + (SLOTS - 1) * step, (it + SLOTS - 1) % SLOTS);
-    asm volatile("cp.async.wait_group %0;" ::"n"(SLOTS - 1) : "memory");
-    const uint4* xs = mine + (it % SLOTS) * 2 * nvec;
-    const uint4* gs = xs + nvec;
-    uint64_t sum = 0;
+    const int slot = it & 1;
+    fetch(row + step, slot ^ 1);
+    cp_wait<1>();
+    const bool two = row + 1 < rows;
+    // without a second row the first one is worked on twice, and counted once
+    const uint4* xs[2] = {mine + slot * 4 * nvec, mine + (slot * 4 + (two ? 2 : 0)) * nvec};
+    uint64_t sum[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int k = t + i * tpr;
       if (k < nvec) {
-        const uint4 q = xs[k];
 #pragma unroll
-        for (int e = 0; e < P; ++e) sum = f2add(sum, PV::get(q, e));
-      }
-    }
-    Share sh;
-    sh.n = share;
-    sh.m = share > 0.f ? warp_sum(f2sum(sum)) / share : 0.f;
-    uint64_t m2 = 0, sa = 0, sax = 0, nm = f2dup(-sh.m);
+        for (int r = 0; r < 2; ++r) {
+          const uint4 q = xs[r][k];
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int k = t + i * tpr;
-      if (k < nvec) {
-        const uint4 q = xs[k], h = gs[k];
-        uint64_t wv[P];
-        load_param<P>(w + (int64_t)k * N, wv);
-#pragma unroll
-        for (int e = 0; e < P; ++e) {
-          const uint64_t d = f2add(PV::get(q, e), nm), a = f2mul(PV::get(h, e), wv[e]);
-          m2 = f2fma(d, d, m2);
-          sa = f2add(sa, a);
-          sax = f2fma(a, d, sax);
+          for (int e = 0; e < P; ++e) sum[r] = f2add(sum[r], PV::get(q, e));
         }
       }
     }
-    sh.m2 = warp_sum(f2sum(m2));
-    sh.a = warp_sum(f2sum(sa));
-    sh.ax = warp_sum(f2sum(sax));
-    if (!WARP) sh = join_shares<true>(sh, rec[it & 1], blockDim.x / 32, C);
-    const float s = 1.0f / sqrtf(sh.m2 / (float)C + eps);
-    if (t == 0) report(sh.m, s, status);
-    nm = f2dup(-sh.m);
-    const uint64_t ss = f2dup(s), c1 = f2dup(-sh.a / (float)C),
-                   c2 = f2dup(-(sh.ax * s / (float)C));
+    // from here to the join a lane's scalars are its half-warp's row's
+    float m = pair_sum(f2sum(sum[0]), f2sum(sum[1]), lane) * inv_n;
+    uint64_t nm[2] = {f2dup(-__shfl_sync(0xffffffffu, m, 0)),
+                      f2dup(-__shfl_sync(0xffffffffu, m, 16))};
+    uint64_t m2[2] = {0, 0}, sa[2] = {0, 0}, sax[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int k = t + i * tpr;
+      if (k < nvec) {
+        uint64_t wv[P];
+        load_param<P>(w + k * N, wv);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint4 q = xs[r][k], h = xs[r][nvec + k];
+#pragma unroll
+          for (int e = 0; e < P; ++e) {
+            const uint64_t d = f2add(PV::get(q, e), nm[r]), a = f2mul(PV::get(h, e), wv[e]);
+            m2[r] = f2fma(d, d, m2[r]);
+            sa[r] = f2add(sa[r], a);
+            sax[r] = f2fma(a, d, sax[r]);
+          }
+        }
+      }
+    }
+    float v2 = pair_sum(f2sum(m2[0]), f2sum(m2[1]), lane);
+    float va = pair_sum(f2sum(sa[0]), f2sum(sa[1]), lane);
+    float vx = pair_sum(f2sum(sax[0]), f2sum(sax[1]), lane);
+    if (!WARP) {
+      if ((lane & 15) == 0) rec[it & 1][lane >> 4][warp] = make_float4(m, v2, va, vx);
+      __syncthreads();
+      const float4 q = nq > 0.f ? rec[it & 1][lane >> 4][lane & 15] : make_float4(0, 0, 0, 0);
+      m = half_sum(nq * q.x) * inv_c;
+      const float d = q.x - m;
+      v2 = half_sum(q.y + nq * d * d);
+      va = half_sum(q.z);
+      vx = half_sum(q.w + d * q.z);
+    }
+    const float s = rsqrtf(v2 * inv_c + eps);
+    if (t == 0 || (t == 16 && two)) report(m, s, status);
+    const float k1 = -va * inv_c, k2 = -vx * s * inv_c;
+    uint64_t ss[2], c1[2], c2[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      nm[r] = f2dup(__shfl_sync(0xffffffffu, -m * s, 16 * r));
+      ss[r] = f2dup(__shfl_sync(0xffffffffu, s, 16 * r));
+      c1[r] = f2dup(__shfl_sync(0xffffffffu, k1, 16 * r));
+      c2[r] = f2dup(__shfl_sync(0xffffffffu, k2, 16 * r));
+    }
     uint4* gr = reinterpret_cast<uint4*>(gx + row * C);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int k = t + i * tpr;
       if (k < nvec) {
-        const uint4 q = xs[k], h = gs[k];
-        uint64_t wv[P], o[P];
-        load_param<P>(w + (int64_t)k * N, wv);
+        uint64_t wv[P];
+        load_param<P>(w + k * N, wv);
 #pragma unroll
-        for (int e = 0; e < P; ++e) {
-          const uint64_t gv = PV::get(h, e), xh = f2mul(f2add(PV::get(q, e), nm), ss);
-          o[e] = f2mul(f2fma(xh, c2, f2fma(gv, wv[e], c1)), ss);
-          gw[i][e] = f2fma(gv, xh, gw[i][e]);
-          gb[i][e] = f2add(gb[i][e], gv);
+        for (int r = 0; r < 2; ++r) {
+          if (r == 0 || two) {
+            const uint4 q = xs[r][k], h = xs[r][nvec + k];
+            uint64_t o[P];
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+              const uint64_t gv = PV::get(h, e), xh = f2fma(PV::get(q, e), ss[r], nm[r]);
+              o[e] = f2mul(f2fma(xh, c2[r], f2fma(gv, wv[e], c1[r])), ss[r]);
+              gw[i][e] = f2fma(gv, xh, gw[i][e]);
+              gb[i][e] = f2add(gb[i][e], gv);
+            }
+            __stcs(gr + r * nvec + k, PV::pack(o));
+          }
         }
-        __stcs(gr + k, PV::pack(o));
       }
     }
   }
   float* sums = WARP ? reinterpret_cast<float*>(ring) : part + (int64_t)blockIdx.x * 2 * C;
-  asm volatile("cp.async.wait_all;" ::: "memory");
+  cp_wait<0>();
   if (WARP) __syncthreads();
   for (int q = 0; q < per; ++q) {
     if (g == q) {
@@ -389,7 +456,8 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_bwd_long(
     int64_t C, float eps, const T* __restrict__ x, const float* __restrict__ w,
     const T* __restrict__ gy, T* __restrict__ gx, float2* __restrict__ stat, int* status) {
   constexpr int N = Vec<T>::N;
-  __shared__ Share rec[32];
+  __shared__ float4 rec[32];
+  __shared__ float num[32];
   const int64_t row = blockIdx.x, nvec = C / N;
   float sum = 0.f, xv[N], gv[N];
   int64_t cnt = 0;
@@ -401,9 +469,9 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_bwd_long(
     sum += q;
     cnt += N;
   }
-  Share sh;
-  sh.n = warp_sum((float)cnt);
-  sh.m = sh.n > 0.f ? warp_sum(sum) / sh.n : 0.f;
+  Share sh = {};
+  const float n = warp_sum((float)cnt);
+  sh.m = warp_sum(sum) * inv_or_0(n);
   float m2 = 0.f, sa = 0.f, sax = 0.f;
   for (int64_t k = threadIdx.x; k < nvec; k += blockDim.x) {
     Vec<T>::load(x + row * C + k * N, xv);
@@ -423,8 +491,8 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_bwd_long(
   sh.m2 = warp_sum(m2);
   sh.a = warp_sum(sa);
   sh.ax = warp_sum(sax);
-  sh = join_shares<true>(sh, rec, blockDim.x / 32, C);
-  const float s = 1.0f / sqrtf(sh.m2 / (float)C + eps);
+  sh = join_shares(n, sh, rec, num, C);
+  const float s = rsqrtf(sh.m2 / (float)C + eps);
   const float c1 = sh.a / (float)C, c2 = sh.ax * s / (float)C;
   if (threadIdx.x == 0) {
     report(sh.m, s, status);
@@ -510,8 +578,8 @@ int sm_count() {
 int round32(int64_t v) { return (int)((v + 31) / 32 * 32); }
 
 // Partial rows of grad_weight / grad_bias: the workspace is sized for this many.
-constexpr int kMaxParts = 320;
-constexpr int64_t kBwdChannels = 16384;  // longer rows take the walks over memory
+constexpr int kMaxParts = 480;
+constexpr int64_t kLongRow = 56 * 1024;  // bytes of x and gy: longer rows are walked in memory
 
 template <typename T>
 cudaError_t fwd(int64_t rows, int64_t C, float eps, const T* x, const float* w, const float* b,
@@ -523,27 +591,28 @@ cudaError_t fwd(int64_t rows, int64_t C, float eps, const T* x, const float* w, 
   }
   if (nvec <= 8 * 32) {
     const unsigned grid = (unsigned)((rows + 3) / 4);
-    auto kern = nvec <= 32   ? k_norm_fwd<T, 1, true>
-                : nvec <= 64 ? k_norm_fwd<T, 2, true>
-                : nvec <= 128 ? k_norm_fwd<T, 4, true>
-                              : k_norm_fwd<T, 8, true>;
+    auto kern = nvec <= 32    ? k_norm_fwd<T, 1, true, 128>
+                : nvec <= 64  ? k_norm_fwd<T, 2, true, 128>
+                : nvec <= 128 ? k_norm_fwd<T, 4, true, 128>
+                              : k_norm_fwd<T, 8, true, 128>;
     return launch_after(kern, grid, 128, 0, 1, s, rows, C, eps, x, w, b, y, st);
   }
-  return launch_after(k_norm_fwd<T, 8, false>, (unsigned)rows, round32((nvec + 7) / 8), 0, 1, s,
-                      rows, C, eps, x, w, b, y, st);
+  auto kern = nvec <= 8 * 256 ? k_norm_fwd<T, 8, false, 256> : k_norm_fwd<T, 8, false, 512>;
+  return launch_after(kern, (unsigned)rows, round32((nvec + 7) / 8), 0, 1, s, rows, C, eps, x, w, b,
+                      y, st);
 }
 
-template <typename T, int VPT, bool WARP, int SLOTS, int MAXT, int PERSM>
+template <typename T, int VPT, bool WARP, int MAXT, int PERSM>
 cudaError_t bwd_rows(int64_t rows, int64_t C, float eps, const T* x, const float* w, const T* gy,
                      T* gx, float* part, int threads, int* nparts, int* st, cudaStream_t s) {
   const int per = WARP ? threads / 32 : 1;
-  const size_t slot = (size_t)2 * C * sizeof(T), sum = WARP ? (size_t)2 * C * 4 : 0;
-  const size_t ring = per * SLOTS * slot, sm = ring > sum ? ring : sum;
-  const int64_t groups = (rows + per - 1) / per;
+  const size_t ring = (size_t)per * 8 * C * sizeof(T);
+  const size_t sum = WARP ? (size_t)2 * C * 4 : 0, sm = ring > sum ? ring : sum;
+  const int64_t groups = (rows + 2 * per - 1) / (2 * per);
   int64_t g = (int64_t)sm_count() * PERSM;
   if (g > kMaxParts) g = kMaxParts;
   *nparts = (int)(groups < g ? groups : g);
-  auto kern = k_norm_bwd<T, VPT, WARP, SLOTS, MAXT, PERSM>;
+  auto kern = k_norm_bwd<T, VPT, WARP, MAXT, PERSM>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
   if (e != cudaSuccess) return e;
@@ -552,19 +621,18 @@ cudaError_t bwd_rows(int64_t rows, int64_t C, float eps, const T* x, const float
 }
 
 // 32 channels per thread: rows of up to 1024 channels on one warp, longer ones on
-// a CTA of which two fit an SM (up to 8192 channels in bf16, 4778 in fp32) or
-// one; three rows in the ring where they fit (an fp32 row pair of 16384 channels
-// takes 128 KB: one).
+// a CTA of which two fit an SM (up to 7168 channels in bf16, 3584 in fp32) or one
+// (twice that); what is longer does not fit the ring.
 template <typename T>
 cudaError_t bwd(int64_t rows, int64_t C, float eps, const T* x, const float* w, const T* gy, T* gx,
                 float* gw, float* gb, void* ws, int* st, cudaStream_t s) {
   constexpr int V = 32 / Vec<T>::N;  // vectors of a thread
-  const int64_t nvec = C / Vec<T>::N;
+  const int64_t nvec = C / Vec<T>::N, row = 2 * C * (int64_t)sizeof(T);  // x and gy
   float* part = (float*)ws;
   int nparts = 0;
   cudaError_t e;
   const int threads = round32((nvec + V - 1) / V);
-  if (C > kBwdChannels) {
+  if (row > kLongRow) {
     float2* stat = (float2*)(part + (int64_t)kMaxParts * 2 * C);
     k_norm_bwd_long<T><<<(unsigned)rows, kMaxThreads, 0, s>>>(C, eps, x, w, gy, gx, stat, st);
     e = cudaGetLastError();
@@ -574,17 +642,15 @@ cudaError_t bwd(int64_t rows, int64_t C, float eps, const T* x, const float* w, 
     k_norm_bwd_cols<T><<<grid, 256, 0, s>>>(rows, C, x, gy, stat, part);
     e = cudaGetLastError();
   } else if (C <= 256) {
-    e = bwd_rows<T, V / 4, true, 3, 256, 2>(rows, C, eps, x, w, gy, gx, part, 256, &nparts, st, s);
+    e = bwd_rows<T, V / 4, true, 256, 2>(rows, C, eps, x, w, gy, gx, part, 256, &nparts, st, s);
   } else if (C <= 512) {
-    e = bwd_rows<T, V / 2, true, 3, 256, 2>(rows, C, eps, x, w, gy, gx, part, 256, &nparts, st, s);
+    e = bwd_rows<T, V / 2, true, 128, 3>(rows, C, eps, x, w, gy, gx, part, 128, &nparts, st, s);
   } else if (C <= 1024) {
-    e = bwd_rows<T, V, true, 3, 128, 2>(rows, C, eps, x, w, gy, gx, part, 128, &nparts, st, s);
-  } else if (threads <= 256 && 3 * 2 * C * sizeof(T) <= 112 * 1024) {
-    e = bwd_rows<T, V, false, 3, 256, 2>(rows, C, eps, x, w, gy, gx, part, threads, &nparts, st, s);
-  } else if (3 * 2 * C * sizeof(T) <= 224 * 1024) {
-    e = bwd_rows<T, V, false, 3, 512, 1>(rows, C, eps, x, w, gy, gx, part, threads, &nparts, st, s);
+    e = bwd_rows<T, V, true, 96, 2>(rows, C, eps, x, w, gy, gx, part, 96, &nparts, st, s);
+  } else if (row <= 28 * 1024 && threads <= 256) {
+    e = bwd_rows<T, V, false, 256, 2>(rows, C, eps, x, w, gy, gx, part, threads, &nparts, st, s);
   } else {
-    e = bwd_rows<T, V, false, 1, 512, 1>(rows, C, eps, x, w, gy, gx, part, threads, &nparts, st, s);
+    e = bwd_rows<T, V, false, 512, 1>(rows, C, eps, x, w, gy, gx, part, threads, &nparts, st, s);
   }
   if (e != cudaSuccess) return e;
   const int64_t cols = 2 * C / 4;
@@ -595,9 +661,8 @@ cudaError_t bwd(int64_t rows, int64_t C, float eps, const T* x, const float* w, 
 }  // namespace
 
 size_t norm_bwd_workspace_bytes(int64_t rows, int64_t C, int dtype) {
-  (void)dtype;
-  const size_t part = (size_t)kMaxParts * 2 * C * 4;
-  return part + (C > kBwdChannels ? (size_t)rows * sizeof(float2) : 0);
+  const int64_t row = 2 * C * (dtype == MHC_DTYPE_BF16 ? 2 : 4);
+  return (size_t)kMaxParts * 2 * C * 4 + (row > kLongRow ? (size_t)rows * sizeof(float2) : 0);
 }
 
 cudaError_t norm_fwd_dispatch(int dtype, int64_t rows, int64_t C, float eps, const void* x,
