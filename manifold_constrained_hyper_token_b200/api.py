@@ -13,7 +13,6 @@ past the end of an allocation.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
@@ -447,18 +446,55 @@ def _rows(x, what="x"):
     return x.shape
 
 
-@contextlib.contextmanager
+class _Here:
+    """Context of a call on the current device's current stream: nothing to switch, and
+    switching anyway costs more than a small kernel."""
+    __slots__ = ("handle",)
+
+    def __init__(self, handle):
+        self.handle = handle
+
+    def __enter__(self):
+        return self.handle
+
+    def __exit__(self, *exc):
+        return False
+
+
+class _There(torch.cuda.StreamContext):
+    """Context of a call on another stream or device."""
+
+    def __enter__(self):
+        super().__enter__()
+        return self.stream.cuda_stream
+
+
 def _on_stream(x, stream):
     """x's device and the call's stream made current: tensors created inside belong to
-    that stream, and the launch goes to x's device whatever device was current.  Yields
-    the stream."""
+    that stream, and the launch goes to x's device whatever device was current.  Gives the
+    stream's handle."""
     if not x.is_cuda:
         raise ValueError("libmhc takes CUDA tensors only")
-    s = torch.cuda.current_stream(x.device) if stream is None else stream
-    if s.device != x.device:
-        raise ValueError(f"stream: on {s.device}, the call runs on {x.device}")
-    with torch.cuda.stream(s):
-        yield s
+    dev = x.device
+    if stream is None:
+        if dev.index == torch.cuda.current_device():
+            return _Here(torch._C._cuda_getCurrentRawStream(dev.index))
+        return _There(torch.cuda.current_stream(dev))
+    if stream.device != dev:
+        raise ValueError(f"stream: on {stream.device}, the call runs on {dev}")
+    return _There(stream)
+
+
+def _ws(t, device):
+    """A workspace that was passed in: on the call's device, its bytes in one piece."""
+    _on(t, device, "workspace")
+    if t is not None and not t.is_contiguous():
+        raise ValueError("workspace: libmhc takes contiguous tensors only")
+
+
+def _a(t):
+    """Address of a tensor that has been checked, None for one left out."""
+    return None if t is None else t.data_ptr()
 
 
 def _norm_params(x, eps):
@@ -481,8 +517,8 @@ def mhc_layer_norm(x, weight, bias=None, *, eps: float = 1e-6, out=None, dev_sta
     _fits(dev_status, 1, torch.int32, x.device, "dev_status")
     with _on_stream(x, stream) as s:
         y = torch.empty_like(x) if out is None else out
-        st = _lib.load().mhc_layer_norm(ctypes.byref(p), _p(x), _p(weight), _p(bias), _p(y),
-                                        _p(dev_status), _stream(s))
+        st = _lib.load().mhc_layer_norm(ctypes.byref(p), _a(x), _a(weight), _a(bias), _a(y),
+                                        _a(dev_status), s)
     _check(st, "mhc_layer_norm")
     return y
 
@@ -508,7 +544,7 @@ def mhc_layer_norm_backward(x, weight, grad_y, *, eps: float = 1e-6, out=None, w
                                       ("grad_x", "grad_weight", "grad_bias")):
             _shaped(t, shape, dt, x.device, what)
     _fits(dev_status, 1, torch.int32, x.device, "dev_status")
-    _on(workspace, x.device, "workspace")
+    _ws(workspace, x.device)
     lib = _lib.load()
     with _on_stream(x, stream) as s:
         if out is None:
@@ -517,8 +553,8 @@ def mhc_layer_norm_backward(x, weight, grad_y, *, eps: float = 1e-6, out=None, w
         gx, gw, gb = out
         ws, wsb = _workspace(int(lib.mhc_layer_norm_backward_workspace_size(ctypes.byref(p))),
                              x.device, workspace)
-        st = lib.mhc_layer_norm_backward(ctypes.byref(p), _p(x), _p(weight), _p(grad_y), _p(gx),
-                                         _p(gw), _p(gb), _p(ws), wsb, _p(dev_status), _stream(s))
+        st = lib.mhc_layer_norm_backward(ctypes.byref(p), _a(x), _a(weight), _a(grad_y), _a(gx),
+                                         _a(gw), _a(gb), _a(ws), wsb, _a(dev_status), s)
     _check(st, "mhc_layer_norm_backward")
     return gx, gw, gb
 
@@ -565,14 +601,14 @@ def mhc_ffn(x, w_gate, w_up, w_down, *, act: str = "silu", wait_ns: int = 0, out
     if out is not None:
         _shaped(out, (T, C), x.dtype, x.device, "out")
     _fits(dev_status, 1, torch.int32, x.device, "dev_status")
-    _on(workspace, x.device, "workspace")
+    _ws(workspace, x.device)
     lib = _lib.load()
     with _on_stream(x, stream) as s:
         y = torch.empty_like(x) if out is None else out
         ws, wsb = _workspace(int(lib.mhc_ffn_workspace_size(ctypes.byref(p))), x.device,
                              workspace)
-        st = lib.mhc_ffn(ctypes.byref(p), _p(x), _p(w_gate), _p(w_up), _p(w_down), _p(y), _p(ws),
-                         wsb, _p(dev_status), _stream(s))
+        st = lib.mhc_ffn(ctypes.byref(p), _a(x), _a(w_gate), _a(w_up), _a(w_down), _a(y), _a(ws),
+                         wsb, _a(dev_status), s)
     _check(st, "mhc_ffn")
     return y
 
@@ -590,7 +626,7 @@ def mhc_ffn_backward(x, w_gate, w_up, w_down, grad_y, *, act: str = "silu", wait
                                   ("grad_x", "grad_w_gate", "grad_w_up", "grad_w_down")):
             _shaped(t, shape, x.dtype, x.device, what)
     _fits(dev_status, 1, torch.int32, x.device, "dev_status")
-    _on(workspace, x.device, "workspace")
+    _ws(workspace, x.device)
     lib = _lib.load()
     with _on_stream(x, stream) as s:
         if out is None:
@@ -599,8 +635,8 @@ def mhc_ffn_backward(x, w_gate, w_up, w_down, grad_y, *, act: str = "silu", wait
         gx, gwg, gwu, gwd = out
         ws, wsb = _workspace(int(lib.mhc_ffn_backward_workspace_size(ctypes.byref(p))), x.device,
                              workspace)
-        st = lib.mhc_ffn_backward(ctypes.byref(p), _p(x), _p(w_gate), _p(w_up), _p(w_down),
-                                  _p(grad_y), _p(gx), _p(gwg), _p(gwu), _p(gwd), _p(ws), wsb,
-                                  _p(dev_status), _stream(s))
+        st = lib.mhc_ffn_backward(ctypes.byref(p), _a(x), _a(w_gate), _a(w_up), _a(w_down),
+                                  _a(grad_y), _a(gx), _a(gwg), _a(gwu), _a(gwd), _a(ws), wsb,
+                                  _a(dev_status), s)
     _check(st, "mhc_ffn_backward")
     return gx, gwg, gwu, gwd

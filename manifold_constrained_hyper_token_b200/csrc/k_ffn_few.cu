@@ -92,8 +92,8 @@ __global__ void __launch_bounds__(few::NT) k_ffn_few(const __grid_constant__ Few
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  tc::grid_release();
   tc::grid_wait();
+  tc::grid_release();
 
   auto give_up = [&]() {
     *abort_flag = 1;
@@ -183,30 +183,51 @@ __global__ void __launch_bounds__(few::NT) k_ffn_few(const __grid_constant__ Few
     else __syncthreads();
     const int64_t row = row0 + r;
     if (row < P.rows) {
-      for (int c = rank; c < cn && c0 + c < P.t; c += parts) {
-        float v[NW];
+      // TOK tokens at a time: the loads from the other CTAs' memory, about a
+      // quarter of a microsecond each, are all under way before the first sum
+      constexpr int TOK = NW == 2 ? 2 : 4;
+      for (int cb = rank; cb < cn && c0 + cb < P.t; cb += TOK * parts) {
+        float ld[TOK][NW][8];
 #pragma unroll
-        for (int i = 0; i < NW; ++i) {
-          const uint32_t at = tc::smem_u32(part + (i * cn + c) * TM + r);
-          v[i] = 0.0f;
-          for (int q = 0; q < parts; ++q) v[i] += tc::ld_cluster_f32(tc::map_cta(at, q));
-        }
-        const int64_t o = (c0 + c) * P.rows + row;
-        if (E == FEW_STORE) {
-          P.o0[o] = __float2bfloat16_rn(v[0]);
-        } else if (E == FEW_GATE) {
-          const float u = v[NW - 1];
-          P.o0[o] = __float2bfloat16_rn(gate<true>(P.act, v[0]) * u);
-          if (P.o1) {
-            P.o1[o] = __float2bfloat16_rn(v[0]);
-            P.o2[o] = __float2bfloat16_rn(u);
+        for (int k = 0; k < TOK; ++k)
+#pragma unroll
+          for (int i = 0; i < NW; ++i)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const int c = cb + k * parts;
+              ld[k][i][q] = 0.0f;
+              if (q < parts && c < cn)
+                ld[k][i][q] = tc::ld_cluster_f32(
+                    tc::map_cta(tc::smem_u32(part + (i * cn + c) * TM + r), q));
+            }
+#pragma unroll
+        for (int k = 0; k < TOK; ++k) {
+          const int c = cb + k * parts;
+          if (c >= cn || c0 + c >= P.t) break;
+          float v[NW];
+#pragma unroll
+          for (int i = 0; i < NW; ++i) {
+            v[i] = ld[k][i][0];
+#pragma unroll
+            for (int q = 1; q < 8; ++q) v[i] += ld[k][i][q];
           }
-        } else {
-          const float g = __bfloat162float(P.g[o]), u = __bfloat162float(P.u[o]);
-          float h, dh;
-          gate_both<true>(P.act, g, h, dh);
-          P.o0[o] = __float2bfloat16_rn(v[0] * u * dh);
-          P.o1[o] = __float2bfloat16_rn(v[0] * h);
+          const int64_t o = (c0 + c) * P.rows + row;
+          if (E == FEW_STORE) {
+            P.o0[o] = __float2bfloat16_rn(v[0]);
+          } else if (E == FEW_GATE) {
+            const float u = v[NW - 1];
+            P.o0[o] = __float2bfloat16_rn(gate<true>(P.act, v[0]) * u);
+            if (P.o1) {
+              P.o1[o] = __float2bfloat16_rn(v[0]);
+              P.o2[o] = __float2bfloat16_rn(u);
+            }
+          } else {
+            const float g = __bfloat162float(P.g[o]), u = __bfloat162float(P.u[o]);
+            float h, dh;
+            gate_both<true>(P.act, g, h, dh);
+            P.o0[o] = __float2bfloat16_rn(v[0] * u * dh);
+            P.o1[o] = __float2bfloat16_rn(v[0] * h);
+          }
         }
       }
     }

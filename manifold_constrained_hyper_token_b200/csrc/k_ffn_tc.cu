@@ -80,6 +80,7 @@ struct GemmArgs {
   int64_t M, N;           // rows and columns of D (columns of one product for GATE, KEEP)
   const void *g, *u;      // EPI_DGATE
   int act;
+  bool beside;            // needs nothing from the kernel before it
   int* status;
   uint64_t wait_ns;
 };
@@ -234,8 +235,8 @@ __global__ void __launch_bounds__(ftc::NT, 1)
   __syncthreads();
   tc::cluster_sync();  // the partner's barriers exist
   tc::tc_fence_after();
+  if (!P.beside) tc::grid_wait();
   tc::grid_release();
-  tc::grid_wait();
   const uint32_t tmem = *tmem_slot;
 
   auto give_up = [&]() {
@@ -479,6 +480,7 @@ __global__ void __launch_bounds__(ftc::NT, 1)
     tc::tc_fence_after();
     tc::tmem_dealloc2(tmem, 512);
   }
+  if (P.beside) tc::grid_wait();
 }
 
 // [rows][cols] fp32 -> three bf16 planes of the same shape.
@@ -681,23 +683,28 @@ cudaError_t bwd(const Ffn& f, void* gx, void* gwg, void* gwu, void* gwd, void* a
     P.u = u;
     TRY((launch<EPI_DGATE, false, true, F32>(P, {GY, {WD}, f.C}, s)));
   }
-  {
-    GemmArgs P = base_args(f, 1, f.C, f.F);
-    TRY(result_map(&P.d[0], {gwd, f.C, f.F, 1, F32}));
-    TRY((launch<EPI_STORE, true, true, F32>(P, {GY, {A}, f.t}, s)));
+  // the rest needs only what is finished when the next kernel starts: the three
+  // run beside one another, each filling the SMs that the one before leaves idle
+  if (few) {
+    TRY(few_grad_x(f.few(), d, gx, s));
+  } else {
+    GemmArgs P = base_args(f, 2, f.t, f.C);
+    TRY(result_map(&P.d[0], {gx, f.t, f.C, 1, F32}));
+    TRY((launch<EPI_STORE, false, true, F32>(P, {D, {WG, WU}, f.F}, s)));
   }
   {
     GemmArgs P = base_args(f, 1, f.F, f.C);
     P.nz = 2;
     P.zplanes = np;
+    P.beside = true;
     TRY(result_map(&P.d[0], {gwg, f.F, f.C, 1, F32}));
     TRY(result_map(&P.d[1], {gwu, f.F, f.C, 1, F32}));
     TRY((launch<EPI_STORE, true, true, F32>(P, {D, {X}, f.t}, s)));
   }
-  if (few) return few_grad_x(f.few(), d, gx, s);
-  GemmArgs P = base_args(f, 2, f.t, f.C);
-  TRY(result_map(&P.d[0], {gx, f.t, f.C, 1, F32}));
-  return launch<EPI_STORE, false, true, F32>(P, {D, {WG, WU}, f.F}, s);
+  GemmArgs P = base_args(f, 1, f.C, f.F);
+  P.beside = true;
+  TRY(result_map(&P.d[0], {gwd, f.C, f.F, 1, F32}));
+  return launch<EPI_STORE, true, true, F32>(P, {GY, {A}, f.t}, s);
 }
 
 size_t up(size_t v) { return (v + 255) / 256 * 256; }

@@ -19,8 +19,12 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Programmatic dependent launch: the next kernel of the stream may be set up from
-// here on / everything before this kernel in its stream has finished.
+// Programmatic dependent launch.  grid_release: the next kernel of the stream may
+// start from here on.  grid_wait: the kernel before this one in the stream has
+// finished (and so has all that it waited for itself).  A kernel that releases
+// after its wait lets the next one run beside it: a next kernel that needs nothing
+// from it may work at once and call grid_wait last, before it ends, so that the
+// end of a kernel still means the end of all before it.
 __device__ __forceinline__ void grid_release() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

@@ -221,6 +221,9 @@ def test_other_arguments_checked(mhc):
             b[call](a, dev_status=torch.zeros(1))
     with pytest.raises(ValueError, match="^workspace: on meta"):
         b["ffn"](a, workspace=torch.empty(8, dtype=torch.uint8, device="meta"))
+    for call in ("ffn", "ffn_bwd", "norm_bwd"):
+        with pytest.raises(ValueError, match="^workspace: "):
+            b[call](a, workspace=torch.empty(1, dtype=torch.uint8).expand(1 << 20))
     for f in (mhc.mhc_ffn_workspace_size, mhc.mhc_ffn_backward_workspace_size):
         with pytest.raises(ValueError):
             f(4, 8, 8, torch.float16)
