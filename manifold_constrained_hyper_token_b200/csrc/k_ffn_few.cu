@@ -49,6 +49,14 @@ struct FewP {
   uint64_t wait_ns;
 };
 
+__device__ __forceinline__ float lo_bf(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_bf(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                            *reinterpret_cast<const uint32_t*>(&b));
+}
+
 template <FewEpi E, bool MN>
 __global__ void __launch_bounds__(few::NT) k_ffn_few(const __grid_constant__ FewP P) {
   using namespace few;
@@ -181,53 +189,64 @@ __global__ void __launch_bounds__(few::NT) k_ffn_few(const __grid_constant__ Few
     }
     if (parts > 1) tc::cluster_sync();
     else __syncthreads();
-    const int64_t row = row0 + r;
+    // a warp per token, four consecutive rows per lane (rows come in eights)
+    const int64_t row = row0 + 4 * lane;
     if (row < P.rows) {
-      // TOK tokens at a time: the loads from the other CTAs' memory, about a
-      // quarter of a microsecond each, are all under way before the first sum
-      constexpr int TOK = NW == 2 ? 2 : 4;
-      for (int cb = rank; cb < cn && c0 + cb < P.t; cb += TOK * parts) {
-        float ld[TOK][NW][8];
+      for (int c = rank + parts * warp; c < cn && c0 + c < P.t; c += parts * 4) {
+        const int64_t o = (c0 + c) * P.rows + row;
+        // every load is under way before the first sum: one from another CTA takes
+        // about a quarter of a microsecond
+        float4 ld[NW][8];
+        uint2 gq = make_uint2(0, 0), uq = gq;
+        if (E == FEW_DGATE) {
+          gq = *reinterpret_cast<const uint2*>(P.g + o);
+          uq = *reinterpret_cast<const uint2*>(P.u + o);
+        }
 #pragma unroll
-        for (int k = 0; k < TOK; ++k)
+        for (int i = 0; i < NW; ++i) {
+          const uint32_t at = tc::smem_u32(part + (i * cn + c) * TM + 4 * lane);
 #pragma unroll
-          for (int i = 0; i < NW; ++i)
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const int c = cb + k * parts;
-              ld[k][i][q] = 0.0f;
-              if (q < parts && c < cn)
-                ld[k][i][q] = tc::ld_cluster_f32(
-                    tc::map_cta(tc::smem_u32(part + (i * cn + c) * TM + r), q));
-            }
-#pragma unroll
-        for (int k = 0; k < TOK; ++k) {
-          const int c = cb + k * parts;
-          if (c >= cn || c0 + c >= P.t) break;
-          float v[NW];
-#pragma unroll
-          for (int i = 0; i < NW; ++i) {
-            v[i] = ld[k][i][0];
-#pragma unroll
-            for (int q = 1; q < 8; ++q) v[i] += ld[k][i][q];
+          for (int q = 0; q < 8; ++q) {
+            ld[i][q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (q < parts) ld[i][q] = tc::ld_cluster_f32x4(tc::map_cta(at, q));
           }
-          const int64_t o = (c0 + c) * P.rows + row;
-          if (E == FEW_STORE) {
-            P.o0[o] = __float2bfloat16_rn(v[0]);
-          } else if (E == FEW_GATE) {
-            const float u = v[NW - 1];
-            P.o0[o] = __float2bfloat16_rn(gate<true>(P.act, v[0]) * u);
-            if (P.o1) {
-              P.o1[o] = __float2bfloat16_rn(v[0]);
-              P.o2[o] = __float2bfloat16_rn(u);
-            }
-          } else {
-            const float g = __bfloat162float(P.g[o]), u = __bfloat162float(P.u[o]);
+        }
+        float v[NW][4];
+#pragma unroll
+        for (int i = 0; i < NW; ++i) {
+          v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.0f;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            v[i][0] += ld[i][q].x;
+            v[i][1] += ld[i][q].y;
+            v[i][2] += ld[i][q].z;
+            v[i][3] += ld[i][q].w;
+          }
+        }
+        if (E == FEW_STORE) {
+          store4(P.o0 + o, v[0]);
+        } else if (E == FEW_GATE) {
+          float a[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) a[k] = gate<true>(P.act, v[0][k]) * v[NW - 1][k];
+          store4(P.o0 + o, a);
+          if (P.o1) {
+            store4(P.o1 + o, v[0]);
+            store4(P.o2 + o, v[NW - 1]);
+          }
+        } else {
+          const float g[4] = {lo_bf(gq.x), hi_bf(gq.x), lo_bf(gq.y), hi_bf(gq.y)};
+          const float u[4] = {lo_bf(uq.x), hi_bf(uq.x), lo_bf(uq.y), hi_bf(uq.y)};
+          float dg[4], du[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
             float h, dh;
-            gate_both<true>(P.act, g, h, dh);
-            P.o0[o] = __float2bfloat16_rn(v[0] * u * dh);
-            P.o1[o] = __float2bfloat16_rn(v[0] * h);
+            gate_both<true>(P.act, g[k], h, dh);
+            dg[k] = v[0][k] * u[k] * dh;
+            du[k] = v[0][k] * h;
           }
+          store4(P.o0 + o, dg);
+          store4(P.o1 + o, du);
         }
       }
     }
