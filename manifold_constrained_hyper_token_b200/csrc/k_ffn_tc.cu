@@ -337,12 +337,14 @@ __global__ void __launch_bounds__(ftc::NT, 1)
     }
   } else if (warp >= 4) {
     // ----------------------------------------------------------- epilogue
-    // 32 columns at a time, staged as boxes of this warp's 32 rows and stored by
-    // TMA; SETS of boxes in turn.  The loops stay rolled: in a small problem the
+    // 32 or 64 columns at a time, staged as boxes of this warp's 32 rows and stored
+    // by TMA; SETS of boxes in turn.  The loops stay rolled: in a small problem the
     // first pass over the code is a pass through instruction-cache misses.
     constexpr int NB = F32 ? 3 : 1;  // boxes of one operand
     constexpr int FB = F32 ? FBOX : HBOX;
-    constexpr int SET = E == EPI_STORE ? FB
+    constexpr bool WIDE = E == EPI_STORE && !F32;  // plain bf16: 64 columns at a time
+    constexpr int SET = WIDE ? 2 * HBOX
+                        : E == EPI_STORE ? FB
                         : E == EPI_GATE ? NB * HBOX
                         : E == EPI_KEEP ? 2 * FB + NB * HBOX
                                         : 2 * NB * HBOX;
@@ -398,7 +400,7 @@ __global__ void __launch_bounds__(ftc::NT, 1)
             }
           };
 #pragma unroll 1
-          for (int c = 0; c < COLS; c += 32) {
+          for (int c = 0; c < COLS; c += WIDE ? 64 : 32) {
             const int64_t col = (int64_t)ni * COLS + c;
             const bool in = row0 < P.M && col < P.N;
             uint8_t* box = out + (nset++ % SETS) * STEP;
@@ -408,7 +410,15 @@ __global__ void __launch_bounds__(ftc::NT, 1)
             for (int g = 0; g < 2; ++g) {
               const int cg = c + 16 * g;
               float v[16];
-              if (E == EPI_STORE) {
+              if (WIDE) {
+                float w[32];
+                tc::tmem_get32(ta + c + 32 * g, w);
+#pragma unroll
+                for (int p = 0; p < 4; ++p)
+                  *reinterpret_cast<uint4*>(box + lane * 128 + (((4 * g + p) ^ (lane & 7)) << 4)) =
+                      make_uint4(bf2(w[8 * p], w[8 * p + 1]), bf2(w[8 * p + 2], w[8 * p + 3]),
+                                 bf2(w[8 * p + 4], w[8 * p + 5]), bf2(w[8 * p + 6], w[8 * p + 7]));
+              } else if (E == EPI_STORE) {
                 sums(cg, v);
                 put_value<F32>(box, lane, g, v);
               } else if (DUAL) {
@@ -526,14 +536,17 @@ cudaError_t operand_map(CUtensorMap* m, const Mat& x, bool mn, int rows) {
   return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x.p, 3, d, s, b,
                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
-cudaError_t result_map(CUtensorMap* m, const Mat& x) {
+// `value`: a result of the call (bf16: boxes of 64 columns); otherwise what a later
+// product reads (32).
+cudaError_t result_map(CUtensorMap* m, const Mat& x, bool value) {
   const uint64_t e = x.f32 ? 4 : 2;
+  const bool wide = value && !x.f32;
   const uint64_t d[3] = {(uint64_t)x.cols, (uint64_t)x.rows, (uint64_t)x.planes};
   const uint64_t s[2] = {(uint64_t)x.cols * e, (uint64_t)x.cols * x.rows * e};
-  const uint32_t b[3] = {32, 32, 1};
+  const uint32_t b[3] = {wide ? 64u : 32u, 32, 1};
   return make_tmap(m, x.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                    x.p, 3, d, s, b,
-                   x.f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                   x.f32 || wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                    CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 
@@ -641,10 +654,10 @@ template <bool F32> cudaError_t gate_product(const Ffn& f, void* a, void* g, voi
   GemmArgs P = base_args(f, 1, f.t, f.F);
   const Opnds o{{f.x, f.t, f.C, f.np, false},
                 {{f.wg, f.F, f.C, f.np, false}, {f.wu, f.F, f.C, f.np, false}}, f.C};
-  TRY(result_map(&P.d[0], {a, f.t, f.F, f.np, false}));
+  TRY(result_map(&P.d[0], {a, f.t, f.F, f.np, false}, false));
   if (g == nullptr) return launch<EPI_GATE, false, false, F32>(P, o, s);
-  TRY(result_map(&P.d[1], {g, f.t, f.F, 1, F32}));
-  TRY(result_map(&P.d[2], {u, f.t, f.F, 1, F32}));
+  TRY(result_map(&P.d[1], {g, f.t, f.F, 1, F32}, false));
+  TRY(result_map(&P.d[2], {u, f.t, f.F, 1, F32}, false));
   return launch<EPI_KEEP, false, false, F32>(P, o, s);
 }
 
@@ -655,7 +668,7 @@ template <bool F32> cudaError_t fwd(const Ffn& f, void* y, void* a, cudaStream_t
   }
   TRY(gate_product<F32>(f, a, nullptr, nullptr, s));
   GemmArgs P = base_args(f, 1, f.t, f.C);
-  TRY(result_map(&P.d[0], {y, f.t, f.C, 1, F32}));
+  TRY(result_map(&P.d[0], {y, f.t, f.C, 1, F32}, true));
   return launch<EPI_STORE, false, false, F32>(
       P, {{a, f.t, f.F, f.np, false}, {{f.wd, f.C, f.F, f.np, false}}, f.F}, s);
 }
@@ -678,7 +691,7 @@ cudaError_t bwd(const Ffn& f, void* gx, void* gwg, void* gwu, void* gwd, void* a
   } else {
     TRY(gate_product<F32>(f, a, g, u, s));
     GemmArgs P = base_args(f, 1, f.t, f.F);
-    TRY(result_map(&P.d[0], D));
+    TRY(result_map(&P.d[0], D, false));
     P.g = g;
     P.u = u;
     TRY((launch<EPI_DGATE, false, true, F32>(P, {GY, {WD}, f.C}, s)));
@@ -689,7 +702,7 @@ cudaError_t bwd(const Ffn& f, void* gx, void* gwg, void* gwu, void* gwd, void* a
     TRY(few_grad_x(f.few(), d, gx, s));
   } else {
     GemmArgs P = base_args(f, 2, f.t, f.C);
-    TRY(result_map(&P.d[0], {gx, f.t, f.C, 1, F32}));
+    TRY(result_map(&P.d[0], {gx, f.t, f.C, 1, F32}, true));
     TRY((launch<EPI_STORE, false, true, F32>(P, {D, {WG, WU}, f.F}, s)));
   }
   {
@@ -697,13 +710,13 @@ cudaError_t bwd(const Ffn& f, void* gx, void* gwg, void* gwu, void* gwd, void* a
     P.nz = 2;
     P.zplanes = np;
     P.beside = true;
-    TRY(result_map(&P.d[0], {gwg, f.F, f.C, 1, F32}));
-    TRY(result_map(&P.d[1], {gwu, f.F, f.C, 1, F32}));
+    TRY(result_map(&P.d[0], {gwg, f.F, f.C, 1, F32}, true));
+    TRY(result_map(&P.d[1], {gwu, f.F, f.C, 1, F32}, true));
     TRY((launch<EPI_STORE, true, true, F32>(P, {D, {X}, f.t}, s)));
   }
   GemmArgs P = base_args(f, 1, f.C, f.F);
   P.beside = true;
-  TRY(result_map(&P.d[0], {gwd, f.C, f.F, 1, F32}));
+  TRY(result_map(&P.d[0], {gwd, f.C, f.F, 1, F32}, true));
   return launch<EPI_STORE, true, true, F32>(P, {GY, {A}, f.t}, s);
 }
 
