@@ -23,8 +23,10 @@
 // smallest first, and what is left out is below 2^-25 of a product.  The tensor
 // cores' adder cuts instead of rounding, about half a unit of the last place per
 // 16-wide step, which adds up over a long sum (measured: 137 x 2^-24 at k =
-// 5456).  So the fp32 sums leave the accumulator every kChunk k blocks and are
-// added up, rounded, in a third TMEM region.
+// 5456).  That matters for the products of the first planes only, the others being
+// 2^-8 of them and less: those stay in the accumulator to their end, and then the
+// first planes' sums leave it every kChunk k blocks.  What leaves is added up,
+// rounded, in a third TMEM region.
 //
 // Warps of a CTA: 0 TMA; 1 the MMAs (first CTA only); 2 TMEM; 4-7 the epilogue.
 // Both CTAs' copies complete on the first CTA's barriers.  (A thread of the
@@ -47,7 +49,7 @@ constexpr int NS = 6;
 constexpr int NEPI = 4;           // epilogue warps
 constexpr int NT = 256;
 constexpr int BAND = 8;
-constexpr int kChunk = 8;         // fp32: k blocks per stay in an accumulator
+constexpr int kChunk = 8;         // fp32: k blocks per stay of the first planes' products
 constexpr int HBOX = 32 * 64;     // one staged box of results: 32 rows of 32 bf16 ...
 constexpr int FBOX = 32 * 128;    // ... or of 32 fp32
 
@@ -84,6 +86,13 @@ struct GemmArgs {
   int* status;
   uint64_t wait_ns;
 };
+
+// The k blocks of the stay in an accumulator that starts at k block j0 end here.
+template <bool F32> __device__ __forceinline__ int stay_end(int j0, int nk) {
+  if (!F32) return nk;
+  const int minor = nk / 6 * 5;  // the products of lower planes come first
+  return j0 < minor ? minor : nk - j0 < ftc::kChunk ? nk : j0 + ftc::kChunk;
+}
 
 // A tile's place: problem z, row tile, column tile; bands of BAND row tiles, row
 // tiles fastest.
@@ -299,8 +308,8 @@ __global__ void __launch_bounds__(ftc::NT, 1)
       int n = 0;  // accumulators filled so far
       bool ok = true, any = false;
       for (int64_t id = pair; id < tiles && ok; id += npairs) {
-        for (int j0 = 0; j0 < nk && ok; j0 += F32 ? kChunk : nk, ++n) {
-          const int j1 = F32 && j0 + kChunk < nk ? j0 + kChunk : nk;
+        for (int j0 = 0, j1; j0 < nk && ok; j0 = j1, ++n) {
+          j1 = stay_end<F32>(j0, nk);
           const int buf = n & 1;
           if (n >= 2 && !tc::mbar_pipe_wait<true>(tempty(buf), ((uint32_t)(n / 2) & 1u) ^ 1u,
                                                   abort_flag, P.wait_ns)) {
@@ -355,7 +364,6 @@ __global__ void __launch_bounds__(ftc::NT, 1)
     const int q = warp & 3;               // TMEM lane quarter this warp may read
     uint8_t* out = smem + G::OUT_OFF + q * G::OUT;
     const int nk = P.nseg * P.kblocks;
-    const int chunks = F32 ? (nk + kChunk - 1) / kChunk : 1;
     const uint32_t master = tmem + ((uint32_t)(32 * q) << 16) + 2 * TN;
     // a tile's products may rightly take longer than one wait: 4 us per k block more
     const uint64_t tile_ns = P.wait_ns + (uint64_t)nk * 4000;
@@ -365,7 +373,8 @@ __global__ void __launch_bounds__(ftc::NT, 1)
       tile_at(P, id, z, mi, ni);
       const int64_t row0 = (int64_t)mi * TM + rank * HALF + 32 * q, row = row0 + lane;
       bool ok = true;
-      for (int ch = 0; ch < chunks; ++ch, ++n) {
+      for (int j0 = 0, j1; j0 < nk; j0 = j1, ++n) {
+        j1 = stay_end<F32>(j0, nk);
         const int buf = n & 1;
         ok = tc::mbar_pipe_wait<false>(tfull(buf), (uint32_t)(n / 2) & 1u, abort_flag, tile_ns);
         if (!ok && !*abort_flag) give_up();
@@ -373,12 +382,12 @@ __global__ void __launch_bounds__(ftc::NT, 1)
         if (!ok) break;
         tc::tc_fence_after();
         const uint32_t ta = tmem + ((uint32_t)(32 * q) << 16) + buf * TN;
-        if (F32 && ch + 1 < chunks) {
+        if (F32 && j1 < nk) {
           // not the last stay: add it to the sums so far
 #pragma unroll 1
           for (int c = 0; c < TN; c += 16) {
             float v[16], m[16];
-            if (ch == 0) {
+            if (j0 == 0) {
               tc::tmem_get16(ta + c, v);
             } else {
               tc::tmem_get16x2(ta + c, master + c, v, m);
@@ -390,7 +399,7 @@ __global__ void __launch_bounds__(ftc::NT, 1)
         } else {
           // D's columns [c, c + 16)
           auto sums = [&](int c, float (&v)[16]) {
-            if (F32 && chunks > 1) {
+            if (F32) {  // two stays at least: the lower planes', the first planes'
               float m[16];
               tc::tmem_get16x2(ta + c, master + c, v, m);
 #pragma unroll
