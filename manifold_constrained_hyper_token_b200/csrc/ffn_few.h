@@ -18,11 +18,11 @@ struct FewArgs {
 };
 
 // a = act(x wg^T) * (x wu^T) [t][F], and g, u [t][F] unless g is null
-cudaError_t few_gate(const FewArgs& f, void* a, void* g, void* u, cudaStream_t s);
+cudaError_t few_gate(const FewArgs& f, void* a, float* g, float* u, cudaStream_t s);
 // y = a wd^T [t][C]
 cudaError_t few_down(const FewArgs& f, const void* a, void* y, cudaStream_t s);
-// d = (dg, du) [2][t][F] from da = gy wd and g, u (which may be d's memory)
-cudaError_t few_dgate(const FewArgs& f, const void* g, const void* u, void* d, cudaStream_t s);
+// d = (dg, du) [2][t][F] from da = gy wd and g, u
+cudaError_t few_dgate(const FewArgs& f, const float* g, const float* u, void* d, cudaStream_t s);
 // gx = dg wg + du wu [t][C]
 cudaError_t few_grad_x(const FewArgs& f, const void* d, void* gx, cudaStream_t s);
 

@@ -41,16 +41,14 @@ struct FewP {
   int nseg, kblocks;     // GATE: one segment, both maps; else segment s: w[s], plane s of x
   int np, stages, chunk; // tokens rounded up to 16; ring stages; tokens reduced at a time
   int64_t rows, t;       // weight rows; tokens
-  __nv_bfloat16 *o0, *o1, *o2;
-  const __nv_bfloat16 *g, *u;
+  __nv_bfloat16 *o0, *o1;
+  float *g, *u;          // GATE: kept unless null; DGATE: read
   int act;
   uint32_t tmem_cols, acc1;  // columns to allocate; the second accumulator's column
   int* status;
   uint64_t wait_ns;
 };
 
-__device__ __forceinline__ float lo_bf(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi_bf(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 __device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
   const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
   *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
@@ -197,10 +195,10 @@ __global__ void __launch_bounds__(few::NT) k_ffn_few(const __grid_constant__ Few
         // every load is under way before the first sum: one from another CTA takes
         // about a quarter of a microsecond
         float4 ld[NW][8];
-        uint2 gq = make_uint2(0, 0), uq = gq;
+        float4 gq, uq;
         if (E == FEW_DGATE) {
-          gq = *reinterpret_cast<const uint2*>(P.g + o);
-          uq = *reinterpret_cast<const uint2*>(P.u + o);
+          gq = *reinterpret_cast<const float4*>(P.g + o);
+          uq = *reinterpret_cast<const float4*>(P.u + o);
         }
 #pragma unroll
         for (int i = 0; i < NW; ++i) {
@@ -230,13 +228,13 @@ __global__ void __launch_bounds__(few::NT) k_ffn_few(const __grid_constant__ Few
 #pragma unroll
           for (int k = 0; k < 4; ++k) a[k] = gate<true>(P.act, v[0][k]) * v[NW - 1][k];
           store4(P.o0 + o, a);
-          if (P.o1) {
-            store4(P.o1 + o, v[0]);
-            store4(P.o2 + o, v[NW - 1]);
+          if (P.g) {
+            *reinterpret_cast<float4*>(P.g + o) = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
+            *reinterpret_cast<float4*>(P.u + o) =
+                make_float4(v[NW - 1][0], v[NW - 1][1], v[NW - 1][2], v[NW - 1][3]);
           }
         } else {
-          const float g[4] = {lo_bf(gq.x), hi_bf(gq.x), lo_bf(gq.y), hi_bf(gq.y)};
-          const float u[4] = {lo_bf(uq.x), hi_bf(uq.x), lo_bf(uq.y), hi_bf(uq.y)};
+          const float g[4] = {gq.x, gq.y, gq.z, gq.w}, u[4] = {uq.x, uq.y, uq.z, uq.w};
           float dg[4], du[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -340,14 +338,14 @@ using bf16 = __nv_bfloat16;
 
 }  // namespace
 
-cudaError_t few_gate(const FewArgs& f, void* a, void* g, void* u, cudaStream_t s) {
+cudaError_t few_gate(const FewArgs& f, void* a, float* g, float* u, cudaStream_t s) {
   FewP P = base(f, f.F, 1);
   TRY(weight_map(&P.w[0], f.wg, f.F, f.C, false));
   TRY(weight_map(&P.w[1], f.wu, f.F, f.C, false));
   TRY(token_map(&P.x, f.x, f.t, f.C, 1, P.np));
   P.o0 = (bf16*)a;
-  P.o1 = (bf16*)g;
-  P.o2 = (bf16*)u;
+  P.g = g;
+  P.u = u;
   return launch<FEW_GATE, false>(P, f, f.C, s);
 }
 
@@ -359,14 +357,14 @@ cudaError_t few_down(const FewArgs& f, const void* a, void* y, cudaStream_t s) {
   return launch<FEW_STORE, false>(P, f, f.F, s);
 }
 
-cudaError_t few_dgate(const FewArgs& f, const void* g, const void* u, void* d, cudaStream_t s) {
+cudaError_t few_dgate(const FewArgs& f, const float* g, const float* u, void* d, cudaStream_t s) {
   FewP P = base(f, f.F, 1);
   TRY(weight_map(&P.w[0], f.wd, f.C, f.F, true));
   TRY(token_map(&P.x, f.gy, f.t, f.C, 1, P.np));
   P.o0 = (bf16*)d;
   P.o1 = (bf16*)d + f.t * f.F;
-  P.g = (const bf16*)g;
-  P.u = (const bf16*)u;
+  P.g = const_cast<float*>(g);
+  P.u = const_cast<float*>(u);
   return launch<FEW_DGATE, true>(P, f, f.C, s);
 }
 

@@ -18,15 +18,18 @@
 // Tiles go over the pairs in bands of eight row tiles, so that the tiles in
 // flight share operands in L2.
 //
-// fp32 operands come as three bf16 planes each (their exact split, split3); the
-// six products of planes whose orders add up to at most two are taken, the
-// smallest first, and what is left out is below 2^-25 of a product.  The tensor
-// cores' adder cuts instead of rounding, about half a unit of the last place per
-// 16-wide step, which adds up over a long sum (measured: 137 x 2^-24 at k =
-// 5456).  That matters for the products of the first planes only, the others being
-// 2^-8 of them and less: those stay in the accumulator to their end, and then the
-// first planes' sums leave it every kChunk k blocks.  What leaves is added up,
-// rounded, in a third TMEM region.
+// fp32 operands come as three bf16 planes each (their exact split, split3).  A
+// stage brings all planes of a 32-wide k block and six of the nine products of
+// planes are taken, those whose orders add up to at most two; what is left out is
+// below 2^-25 of a product.  The tensor cores' adder cuts instead of rounding,
+// about half a unit of the last place per 16-wide step, which adds up over a long
+// sum (measured: 137 x 2^-24 at k = 5456).  So the first planes' products have
+// accumulators of their own, which they leave every kChunk k blocks to be added
+// up, rounded, in another TMEM region; the other products are 2^-8 of them and
+// less and stay in one accumulator to the end.
+//
+// The backward's g and u are kept in fp32: rounded to bf16 they would put as much
+// error into dg and du as these take from their own rounding.
 //
 // Warps of a CTA: 0 TMA; 1 the MMAs (first CTA only); 2 TMEM; 4-7 the epilogue.
 // Both CTAs' copies complete on the first CTA's barriers.  (A thread of the
@@ -34,6 +37,8 @@
 // release at cluster scope, took about 0.9 us per stage: 600 TFLOP/s in all.)
 // Every wait is bounded as in the other tensor-core kernels: on timeout the
 // kernel records MHC_ERR_TIMEOUT, drains what it issued and returns.
+#include <algorithm>
+
 #include "ffn_common.cuh"
 #include "ffn_few.h"
 #include "mhc_dispatch.h"
@@ -42,26 +47,30 @@
 namespace mhc {
 
 namespace ftc {
-constexpr int TM = 256, TK = 64;  // the pair's rows, and the k block
+constexpr int TM = 256;           // the pair's rows
 constexpr int HALF = 128;         // rows of A that one CTA brings
-constexpr int ABYTES = HALF * TK * 2;
-constexpr int NS = 6;
 constexpr int NEPI = 4;           // epilogue warps
 constexpr int NT = 256;
 constexpr int BAND = 8;
-constexpr int kChunk = 8;         // fp32: k blocks per stay of the first planes' products
-constexpr int HBOX = 32 * 64;     // one staged box of results: 32 rows of 32 bf16 ...
-constexpr int FBOX = 32 * 128;    // ... or of 32 fp32
+constexpr int kChunk = 16;        // fp32: k blocks per stay of the first planes' products
+constexpr int BOX = 32 * 64;      // a staged box of results: 32 rows of 32 bf16 or 16 fp32
 
 template <int TN, bool F32> struct Cfg {
+  static constexpr int TK = F32 ? 32 : 64;              // k block
+  static constexpr int NP = F32 ? 3 : 1;                // planes of an operand
+  static constexpr int NS = F32 ? 4 : 6;                // stages
   static constexpr int BROWS = TN / 2;                  // rows of B that one CTA brings
-  static constexpr int STAGE = ABYTES + BROWS * TK * 2;
+  static constexpr int APLANE = HALF * TK * 2, BPLANE = BROWS * TK * 2;
+  static constexpr int ABYTES = NP * APLANE;
+  static constexpr int STAGE = ABYTES + NP * BPLANE;
   static constexpr int OUT = F32 ? 16384 : 8192;        // staged results per epilogue warp
   static constexpr int OUT_OFF = NS * STAGE;
   static constexpr int BAR_OFF = OUT_OFF + NEPI * OUT;
   static constexpr int SMEM = BAR_OFF + 256 + 1024;
+  // TMEM columns: two accumulators; fp32: the lower planes' products, the sums
+  static constexpr uint32_t MINOR = 2 * TN, SUMS = 3 * TN;
   static_assert(STAGE % 1024 == 0 && SMEM <= 232448, "shared memory");
-  static_assert((F32 ? 3 : 2) * TN <= 512, "TMEM columns");
+  static_assert((F32 ? 4 : 2) * TN <= 512, "TMEM columns");
 };
 }  // namespace ftc
 
@@ -69,18 +78,15 @@ namespace {
 
 enum Epi { EPI_STORE, EPI_GATE, EPI_KEEP, EPI_DGATE };
 
-constexpr int kMaxSegs = 12;
-
-// One launch.  Segment s multiplies plane ap of A's map am by plane bp of B's
-// map bm; all segments of a tile add into one accumulator.
+// One launch: the sum of nseg products into each tile, the s-th of A's planes
+// from s NP on by B's map s.
 struct GemmArgs {
-  CUtensorMap a[2], b[2], d[3];
-  uint8_t am[kMaxSegs], ap[kMaxSegs], bm[kMaxSegs], bp[kMaxSegs];
+  CUtensorMap a, b[2], d[3];
   int nseg, kblocks;
-  int mt, nt, nz;         // tiles of a problem; problems (a plane of A and a map of D each)
+  int mt, nt, nz;         // tiles of a problem; problems (planes of A and a map of D each)
   int zplanes;            // planes of A per problem
   int64_t M, N;           // rows and columns of D (columns of one product for GATE, KEEP)
-  const void *g, *u;      // EPI_DGATE
+  const float *g, *u;     // EPI_DGATE
   int act;
   bool beside;            // needs nothing from the kernel before it
   int* status;
@@ -89,9 +95,7 @@ struct GemmArgs {
 
 // The k blocks of the stay in an accumulator that starts at k block j0 end here.
 template <bool F32> __device__ __forceinline__ int stay_end(int j0, int nk) {
-  if (!F32) return nk;
-  const int minor = nk / 6 * 5;  // the products of lower planes come first
-  return j0 < minor ? minor : nk - j0 < ftc::kChunk ? nk : j0 + ftc::kChunk;
+  return !F32 || nk - j0 < ftc::kChunk ? nk : j0 + ftc::kChunk;
 }
 
 // A tile's place: problem z, row tile, column tile; bands of BAND row tiles, row
@@ -108,23 +112,27 @@ __device__ __forceinline__ void tile_at(const GemmArgs& P, int64_t id, int& z, i
   mi = m0 + (int)(in % rows);
 }
 
-// One operand of a stage: ROWS rows x 64 k.  Stored along k: one box.  Stored
-// along its rows (MN): boxes of 64 rows.
-template <int ROWS, bool MN>
+// One operand of a stage, all its planes: ROWS rows x TK k.  Stored along k: one
+// box [plane][row][k].  Stored along its rows (MN): boxes [plane][k][64 rows].
+template <class G, int ROWS, bool MN>
 __device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* map, uint32_t bar,
                                           int row0, int k0, int plane, uint64_t pol) {
   if (MN) {
 #pragma unroll
     for (int r = 0; r < ROWS; r += 64)
-      tc::tma2_load_3d(dst + r * 128, map, bar, row0 + r, k0, plane, pol);
+      tc::tma2_load_3d(dst + (r / 64) * G::NP * G::TK * 128, map, bar, row0 + r, k0, plane, pol);
   } else {
     tc::tma2_load_3d(dst, map, bar, k0, row0, plane, pol);
   }
 }
-// The descriptor of the k-th 16-wide slice of that operand.
-template <bool MN> __device__ __forceinline__ uint64_t rows_desc(uint32_t base, int k) {
-  return MN ? tc::smem_desc(base + k * 2048, 8192, 1024, tc::SWZ_128B)
-            : tc::smem_desc(base + k * 32, 16, 1024, tc::SWZ_128B);
+// The descriptor of the k-th 16-wide slice of a plane of that operand.
+template <class G, int ROWS, bool MN>
+__device__ __forceinline__ uint64_t rows_desc(uint32_t base, int plane, int k) {
+  if (MN)
+    return tc::smem_desc(base + plane * G::TK * 128 + k * 2048, G::NP * G::TK * 128, 1024,
+                         tc::SWZ_128B);
+  return tc::smem_desc(base + plane * ROWS * G::TK * 2 + k * 32, 16, G::TK * 16,
+                       G::TK == 64 ? tc::SWZ_128B : tc::SWZ_64B);
 }
 
 __device__ __forceinline__ uint32_t bf2(float a, float b) {
@@ -132,20 +140,24 @@ __device__ __forceinline__ uint32_t bf2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Columns [16 g, 16 g + 16) of row `lane` of a staged box: 64-byte rows with the
-// 64-byte swizzle (bf16), 128-byte rows with the 128-byte swizzle (fp32).
+// Row `lane` of a staged box (64-byte rows with the 64-byte swizzle): columns
+// [16 g, 16 g + 16) of 32 bf16, or 16 fp32.
+__device__ __forceinline__ uint4* box_piece(uint8_t* box, int lane, int p) {
+  return reinterpret_cast<uint4*>(box + lane * 64 + ((p ^ ((lane >> 1) & 3)) << 4));
+}
 __device__ __forceinline__ void put_bf16(uint8_t* box, int lane, int g, const float (&v)[16]) {
 #pragma unroll
   for (int p = 0; p < 2; ++p)
-    *reinterpret_cast<uint4*>(box + lane * 64 + (((2 * g + p) ^ ((lane >> 1) & 3)) << 4)) =
+    *box_piece(box, lane, 2 * g + p) =
         make_uint4(bf2(v[8 * p], v[8 * p + 1]), bf2(v[8 * p + 2], v[8 * p + 3]),
                    bf2(v[8 * p + 4], v[8 * p + 5]), bf2(v[8 * p + 6], v[8 * p + 7]));
 }
-__device__ __forceinline__ void put_f32(uint8_t* box, int lane, int g, const float (&v)[16]) {
+__device__ __forceinline__ void put_f32(uint8_t* box, int lane, const float (&v)[16]) {
 #pragma unroll
   for (int p = 0; p < 4; ++p)
-    *reinterpret_cast<float4*>(box + lane * 128 + (((4 * g + p) ^ (lane & 7)) << 4)) =
-        make_float4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
+    *box_piece(box, lane, p) =
+        make_uint4(__float_as_uint(v[4 * p]), __float_as_uint(v[4 * p + 1]),
+                   __float_as_uint(v[4 * p + 2]), __float_as_uint(v[4 * p + 3]));
 }
 // A value that the next product takes as an operand: itself in bf16, or its three
 // planes in three boxes.
@@ -158,38 +170,21 @@ __device__ __forceinline__ void put_operand(uint8_t* box, int lane, int g, const
 #pragma unroll
     for (int i = 0; i < 16; ++i) split3(v[i], h[i], m[i], l[i]);
     put_bf16(box, lane, g, h);
-    put_bf16(box + ftc::HBOX, lane, g, m);
-    put_bf16(box + 2 * ftc::HBOX, lane, g, l);
+    put_bf16(box + ftc::BOX, lane, g, m);
+    put_bf16(box + 2 * ftc::BOX, lane, g, l);
   }
-}
-template <bool F32>
-__device__ __forceinline__ void put_value(uint8_t* box, int lane, int g, const float (&v)[16]) {
-  if (F32) put_f32(box, lane, g, v);
-  else put_bf16(box, lane, g, v);
 }
 
 // 16 columns of this lane's row of g or u, from column col on; what lies past the
 // end is not read.
-template <bool F32>
-__device__ __forceinline__ void row16(const void* base, int64_t row, int64_t col, int64_t M,
+__device__ __forceinline__ void row16(const float* base, int64_t row, int64_t col, int64_t M,
                                       int64_t N, float (&v)[16]) {
-  constexpr int VN = F32 ? 4 : 8;
 #pragma unroll
-  for (int i = 0; i < 16; i += VN) {
-    if (row < M && col + i < N) {
-      if (F32) {
-        const float4 q = *reinterpret_cast<const float4*>((const float*)base + row * N + col + i);
-        v[i] = q.x, v[i + 1] = q.y, v[i + 2] = q.z, v[i + 3] = q.w;
-      } else {
-        float t[8];
-        Vec<__nv_bfloat16>::load((const __nv_bfloat16*)base + row * N + col + i, t);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[i + e] = t[e];
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < VN; ++e) v[i + e] = 0.0f;
-    }
+  for (int i = 0; i < 16; i += 4) {
+    float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (row < M && col + i < N)
+      q = __ldcs(reinterpret_cast<const float4*>(base + row * N + col + i));
+    v[i] = q.x, v[i + 1] = q.y, v[i + 2] = q.z, v[i + 3] = q.w;
   }
 }
 
@@ -198,19 +193,20 @@ __global__ void __launch_bounds__(ftc::NT, 1)
     k_ffn_tc(const __grid_constant__ GemmArgs P) {
   using namespace ftc;
   using G = Cfg<TN, F32>;
-  constexpr int STAGE = G::STAGE, HN = TN / 2;
+  constexpr int STAGE = G::STAGE, NS = G::NS, TK = G::TK, HN = TN / 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~(uintptr_t)1023);
-  // full[NS] empty[NS] tfull[2] tempty[2] fin
+  // full[NS] empty[NS] tfull[2] tempty[2] mempty fin
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + G::BAR_OFF);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * NS + 5);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * NS + 6);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   auto full = [&](int s) { return tc::smem_u32(bars + s); };
   auto empty = [&](int s) { return tc::smem_u32(bars + NS + s); };
   auto tfull = [&](int b) { return tc::smem_u32(bars + 2 * NS + b); };
   auto tempty = [&](int b) { return tc::smem_u32(bars + 2 * NS + 2 + b); };
-  const uint32_t fin_bar = tc::smem_u32(bars + 2 * NS + 4);
+  const uint32_t mempty = tc::smem_u32(bars + 2 * NS + 4);  // fp32: the lower planes' sums
+  const uint32_t fin_bar = tc::smem_u32(bars + 2 * NS + 5);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int rank = (int)tc::cluster_rank();
@@ -227,12 +223,13 @@ __global__ void __launch_bounds__(ftc::NT, 1)
       tc::mbar_init(tfull(b), 1);
       tc::mbar_init(tempty(b), 2 * NEPI);
     }
+    tc::mbar_init(mempty, 2 * NEPI);
     tc::mbar_init(fin_bar, 1);
     *abort_flag = 0;
     tc::mbar_fence_init();
   }
   if (warp == 0 && lane == 0) {
-    tc::tma_prefetch_desc(&P.a[0]);
+    tc::tma_prefetch_desc(&P.a);
     tc::tma_prefetch_desc(&P.b[0]);
     tc::tma_prefetch_desc(&P.d[0]);
   }
@@ -265,9 +262,8 @@ __global__ void __launch_bounds__(ftc::NT, 1)
         const int arow = mi * TM + rank * HALF;
         const int brow = DUAL ? ni * HN : ni * TN + rank * HN;
         for (int sg = 0; sg < P.nseg && ok; ++sg) {
-          const CUtensorMap* am = &P.a[P.am[sg]];
-          const CUtensorMap* bm = &P.b[DUAL ? rank : P.bm[sg]];
-          const int ap = P.ap[sg] + z * P.zplanes, bp = P.bp[sg];
+          const CUtensorMap* bm = &P.b[DUAL ? rank : sg];
+          const int ap = sg * G::NP + z * P.zplanes;
           for (int kb = 0; kb < P.kblocks; ++kb, ++it) {
             const int s = (int)(it % NS);
             if (it >= NS && !tc::mbar_pipe_wait<false>(empty(s), ((uint32_t)(it / NS) & 1u) ^ 1u,
@@ -279,8 +275,8 @@ __global__ void __launch_bounds__(ftc::NT, 1)
             const uint32_t base = tc::smem_u32(smem + s * STAGE);
             if (rank == 0) tc::mbar_arrive_expect_tx(full(s), 2 * STAGE);
             const uint32_t bar = tc::map_cta(full(s), 0);
-            load_rows<HALF, AMN>(base, am, bar, arow, kb * TK, ap, pol);
-            load_rows<HN, BMN>(base + ABYTES, bm, bar, brow, kb * TK, bp, pol);
+            load_rows<G, HALF, AMN>(base, &P.a, bar, arow, kb * TK, ap, pol);
+            load_rows<G, HN, BMN>(base + G::ABYTES, bm, bar, brow, kb * TK, 0, pol);
           }
         }
       }
@@ -307,7 +303,13 @@ __global__ void __launch_bounds__(ftc::NT, 1)
       int64_t it = 0;
       int n = 0;  // accumulators filled so far
       bool ok = true, any = false;
-      for (int64_t id = pair; id < tiles && ok; id += npairs) {
+      uint32_t done = 0;  // tiles
+      for (int64_t id = pair; id < tiles && ok; id += npairs, ++done) {
+        if (F32 && done > 0 &&
+            !tc::mbar_pipe_wait<true>(mempty, (done & 1u) ^ 1u, abort_flag, P.wait_ns)) {
+          give_up();
+          break;
+        }
         for (int j0 = 0, j1; j0 < nk && ok; j0 = j1, ++n) {
           j1 = stay_end<F32>(j0, nk);
           const int buf = n & 1;
@@ -328,10 +330,21 @@ __global__ void __launch_bounds__(ftc::NT, 1)
             }
             tc::tc_fence_after();
             const uint32_t base = tc::smem_u32(smem + s * STAGE);
+            auto mma = [&](uint32_t col, int pa, int pb, int k, bool add) {
+              tc::mma2_bf16(tmem + col, rows_desc<G, HALF, AMN>(base, pa, k),
+                            rows_desc<G, HN, BMN>(base + G::ABYTES, pb, k), idesc, add ? 1u : 0u);
+            };
 #pragma unroll
-            for (int k = 0; k < TK / 16; ++k)
-              tc::mma2_bf16(tmem + buf * TN, rows_desc<AMN>(base, k),
-                            rows_desc<BMN>(base + ABYTES, k), idesc, j > j0 || k > 0 ? 1u : 0u);
+            for (int k = 0; k < TK / 16; ++k) {
+              if (F32) {
+                mma(G::MINOR, 2, 0, k, j > 0 || k > 0);
+                mma(G::MINOR, 1, 1, k, true);
+                mma(G::MINOR, 0, 2, k, true);
+                mma(G::MINOR, 1, 0, k, true);
+                mma(G::MINOR, 0, 1, k, true);
+              }
+              mma(buf * TN, 0, 0, k, j > j0 || k > 0);
+            }
             any = true;
             tc::mma2_commit(empty(s));
           }
@@ -349,22 +362,19 @@ __global__ void __launch_bounds__(ftc::NT, 1)
     // 32 or 64 columns at a time, staged as boxes of this warp's 32 rows and stored
     // by TMA; SETS of boxes in turn.  The loops stay rolled: in a small problem the
     // first pass over the code is a pass through instruction-cache misses.
-    constexpr int NB = F32 ? 3 : 1;  // boxes of one operand
-    constexpr int FB = F32 ? FBOX : HBOX;
+    constexpr int NB = F32 ? 3 : 1;                // boxes of one operand
     constexpr bool WIDE = E == EPI_STORE && !F32;  // plain bf16: 64 columns at a time
-    constexpr int SET = WIDE ? 2 * HBOX
-                        : E == EPI_STORE ? FB
-                        : E == EPI_GATE ? NB * HBOX
-                        : E == EPI_KEEP ? 2 * FB + NB * HBOX
-                                        : 2 * NB * HBOX;
+    constexpr int SET = E == EPI_STORE  ? 2 * BOX
+                        : E == EPI_GATE ? NB * BOX
+                        : E == EPI_KEEP ? (2 + NB) * BOX
+                                        : 2 * NB * BOX;
     constexpr int SETS = G::OUT / SET > 4 ? 4 : G::OUT / SET;
-    constexpr int STEP = SET % 1024 ? SET + 1024 - SET % 1024 : SET;
-    static_assert(SETS >= 1 && STEP * SETS <= G::OUT, "staged results");
+    static_assert(SETS >= 1, "staged results");
     constexpr int COLS = DUAL ? HN : TN;  // columns of D's tile
     const int q = warp & 3;               // TMEM lane quarter this warp may read
     uint8_t* out = smem + G::OUT_OFF + q * G::OUT;
     const int nk = P.nseg * P.kblocks;
-    const uint32_t master = tmem + ((uint32_t)(32 * q) << 16) + 2 * TN;
+    const uint32_t sums = tmem + ((uint32_t)(32 * q) << 16) + G::SUMS;
     // a tile's products may rightly take longer than one wait: 4 us per k block more
     const uint64_t tile_ns = P.wait_ns + (uint64_t)nk * 4000;
     int n = 0, nset = 0;
@@ -382,37 +392,41 @@ __global__ void __launch_bounds__(ftc::NT, 1)
         if (!ok) break;
         tc::tc_fence_after();
         const uint32_t ta = tmem + ((uint32_t)(32 * q) << 16) + buf * TN;
-        if (F32 && j1 < nk) {
-          // not the last stay: add it to the sums so far
+        if (F32) {
+          // this stay's sums to those before it; at the end the lower planes' too
 #pragma unroll 1
           for (int c = 0; c < TN; c += 16) {
             float v[16], m[16];
             if (j0 == 0) {
               tc::tmem_get16(ta + c, v);
             } else {
-              tc::tmem_get16x2(ta + c, master + c, v, m);
+              tc::tmem_get16x2(ta + c, sums + c, v, m);
 #pragma unroll
               for (int i = 0; i < 16; ++i) v[i] += m[i];
             }
-            tc::tmem_put16(master + c, v);
+            if (j1 == nk) {
+              tc::tmem_get16(sums + c - G::SUMS + G::MINOR, m);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] += m[i];
+            }
+            tc::tmem_put16(sums + c, v);
           }
-        } else {
-          // D's columns [c, c + 16)
-          auto sums = [&](int c, float (&v)[16]) {
-            if (F32) {  // two stays at least: the lower planes', the first planes'
-              float m[16];
-              tc::tmem_get16x2(ta + c, master + c, v, m);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] += m[i];
-            } else {
-              tc::tmem_get16(ta + c, v);
-            }
-          };
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            tc::mbar_arrive_cluster(tc::map_cta(tempty(buf), 0));
+            if (j1 == nk) tc::mbar_arrive_cluster(tc::map_cta(mempty, 0));
+          }
+        }
+        if (j1 == nk) {
+          const uint32_t at = F32 ? sums : ta;  // D's columns
 #pragma unroll 1
           for (int c = 0; c < COLS; c += WIDE ? 64 : 32) {
             const int64_t col = (int64_t)ni * COLS + c;
             const bool in = row0 < P.M && col < P.N;
-            uint8_t* box = out + (nset++ % SETS) * STEP;
+            uint8_t* box = out + (nset++ % SETS) * SET;
+            const uint32_t bu = tc::smem_u32(box);
+            const int cc = (int)col, rr = (int)row0;
             if (lane == 0) tc::bulk_wait_read<SETS - 1>();
             __syncwarp();
 #pragma unroll 1
@@ -421,31 +435,46 @@ __global__ void __launch_bounds__(ftc::NT, 1)
               float v[16];
               if (WIDE) {
                 float w[32];
-                tc::tmem_get32(ta + c + 32 * g, w);
+                tc::tmem_get32(at + c + 32 * g, w);
 #pragma unroll
                 for (int p = 0; p < 4; ++p)
                   *reinterpret_cast<uint4*>(box + lane * 128 + (((4 * g + p) ^ (lane & 7)) << 4)) =
                       make_uint4(bf2(w[8 * p], w[8 * p + 1]), bf2(w[8 * p + 2], w[8 * p + 3]),
                                  bf2(w[8 * p + 4], w[8 * p + 5]), bf2(w[8 * p + 6], w[8 * p + 7]));
               } else if (E == EPI_STORE) {
-                sums(cg, v);
-                put_value<F32>(box, lane, g, v);
+                tc::tmem_get16(at + cg, v);
+                put_f32(box + g * BOX, lane, v);
               } else if (DUAL) {
                 float u[16];
-                sums(cg, v);
-                sums(HN + cg, u);
+                tc::tmem_get16x2(at + cg, at + HN + cg, v, u);
                 if (E == EPI_KEEP) {
-                  put_value<F32>(box, lane, g, v);
-                  put_value<F32>(box + FB, lane, g, u);
+                  // g and u leave in boxes of 16 columns, a in one of 32
+                  if (g == 1) {
+                    if (lane == 0) tc::bulk_wait_read<0>();
+                    __syncwarp();
+                  }
+                  put_f32(box, lane, v);
+                  put_f32(box + BOX, lane, u);
                 }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) v[i] = gate<!F32>(P.act, v[i]) * u[i];
-                put_operand<F32>(box + (E == EPI_KEEP ? 2 * FB : 0), lane, g, v);
+                put_operand<F32>(box + (E == EPI_KEEP ? 2 * BOX : 0), lane, g, v);
+                if (E == EPI_KEEP) {
+                  tc::fence_proxy_async_smem();
+                  __syncwarp();
+                  if (lane == 0) {
+                    if (in && col + 16 * g < P.N) {
+                      tc::tma_store_3d(&P.d[1], bu, cc + 16 * g, rr, 0);
+                      tc::tma_store_3d(&P.d[2], bu + BOX, cc + 16 * g, rr, 0);
+                    }
+                    if (g == 0) tc::bulk_commit();
+                  }
+                }
               } else {
                 float u[16], gv[16];
-                row16<F32>(P.g, row, col + 16 * g, P.M, P.N, gv);
-                row16<F32>(P.u, row, col + 16 * g, P.M, P.N, u);
-                sums(cg, v);
+                row16(P.g, row, col + 16 * g, P.M, P.N, gv);
+                row16(P.u, row, col + 16 * g, P.M, P.N, u);
+                tc::tmem_get16(at + cg, v);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                   float h, dh;
@@ -454,37 +483,36 @@ __global__ void __launch_bounds__(ftc::NT, 1)
                   v[i] *= h;
                 }
                 put_operand<F32>(box, lane, g, u);
-                put_operand<F32>(box + NB * HBOX, lane, g, v);
+                put_operand<F32>(box + NB * BOX, lane, g, v);
               }
             }
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
               if (in) {
-                const uint32_t b = tc::smem_u32(box);
-                const int cc = (int)col, rr = (int)row0;
-                if (E == EPI_STORE) {
-                  tc::tma_store_3d(&P.d[z], b, cc, rr, 0);
+                if (WIDE) {
+                  tc::tma_store_3d(&P.d[z], bu, cc, rr, 0);
+                } else if (E == EPI_STORE) {
+                  tc::tma_store_3d(&P.d[z], bu, cc, rr, 0);
+                  if (col + 16 < P.N) tc::tma_store_3d(&P.d[z], bu + BOX, cc + 16, rr, 0);
                 } else if (E == EPI_DGATE) {
                   for (int pl = 0; pl < 2 * NB; ++pl)
-                    tc::tma_store_3d(&P.d[0], b + pl * HBOX, cc, rr, pl);
+                    tc::tma_store_3d(&P.d[0], bu + pl * BOX, cc, rr, pl);
                 } else {
-                  if (E == EPI_KEEP) {
-                    tc::tma_store_3d(&P.d[1], b, cc, rr, 0);
-                    tc::tma_store_3d(&P.d[2], b + FB, cc, rr, 0);
-                  }
                   for (int pl = 0; pl < NB; ++pl)
-                    tc::tma_store_3d(&P.d[0], b + (E == EPI_KEEP ? 2 * FB : 0) + pl * HBOX, cc, rr,
-                                     pl);
+                    tc::tma_store_3d(&P.d[0], bu + (E == EPI_KEEP ? 2 * BOX : 0) + pl * BOX, cc,
+                                     rr, pl);
                 }
               }
               tc::bulk_commit();
             }
           }
         }
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive_cluster(tc::map_cta(tempty(buf), 0));
+        if (!F32) {
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive_cluster(tc::map_cta(tempty(buf), 0));
+        }
       }
       if (!ok) break;
     }
@@ -502,30 +530,33 @@ __global__ void __launch_bounds__(ftc::NT, 1)
   if (P.beside) tc::grid_wait();
 }
 
-// [rows][cols] fp32 -> three bf16 planes of the same shape.
-__global__ void __launch_bounds__(256) k_split3(int64_t n, const float* __restrict__ v,
-                                                __nv_bfloat16* __restrict__ out) {
-  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n;
-       i += (int64_t)gridDim.x * 256 * 8) {
-    float p[3][8];
+// fp32 arrays of n[i] elements (multiples of 8) -> their three bf16 planes each.
+struct SplitArgs {
+  const float* src[5];
+  __nv_bfloat16* dst[5];
+  int64_t n[5];
+  int count;
+};
+__global__ void __launch_bounds__(256) k_split3(const __grid_constant__ SplitArgs a) {
+  tc::grid_wait();
+  tc::grid_release();
+  for (int q = 0; q < a.count; ++q) {
+    const int64_t n = a.n[q];
+    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n;
+         i += (int64_t)gridDim.x * 256 * 8) {
+      float p[3][8];
 #pragma unroll
-    for (int h = 0; h < 8; h += 4) {
-      const float4 q = __ldcs(reinterpret_cast<const float4*>(v + i + h));
-      const float w[4] = {q.x, q.y, q.z, q.w};
+      for (int h = 0; h < 8; h += 4) {
+        const float4 f = __ldcs(reinterpret_cast<const float4*>(a.src[q] + i + h));
+        const float w[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) split3(w[e], p[0][h + e], p[1][h + e], p[2][h + e]);
+        for (int e = 0; e < 4; ++e) split3(w[e], p[0][h + e], p[1][h + e], p[2][h + e]);
+      }
+#pragma unroll
+      for (int pl = 0; pl < 3; ++pl)
+        *reinterpret_cast<uint4*>(a.dst[q] + pl * n + i) = Vec<__nv_bfloat16>::pack(p[pl]);
     }
-#pragma unroll
-    for (int pl = 0; pl < 3; ++pl)
-      *reinterpret_cast<uint4*>(out + pl * n + i) = Vec<__nv_bfloat16>::pack(p[pl]);
   }
-}
-
-cudaError_t split3_launch(int64_t n, const void* v, void* out, cudaStream_t s) {
-  const int64_t blocks = (n / 8 + 255) / 256;
-  k_split3<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, s>>>(n, (const float*)v,
-                                                                    (__nv_bfloat16*)out);
-  return cudaGetLastError();
 }
 
 // A matrix in memory: [planes][rows][cols], bf16 (operands) or fp32 (results).
@@ -537,42 +568,27 @@ struct Mat {
 };
 
 // mn: the operand's own rows run along the stored columns; otherwise boxes of
-// `rows` rows.
-cudaError_t operand_map(CUtensorMap* m, const Mat& x, bool mn, int rows) {
+// `rows` rows.  np planes at a time.
+cudaError_t operand_map(CUtensorMap* m, const Mat& x, bool mn, int rows, int np) {
+  const uint32_t tk = np == 3 ? 32 : 64;
   const uint64_t d[3] = {(uint64_t)x.cols, (uint64_t)x.rows, (uint64_t)x.planes};
   const uint64_t s[2] = {(uint64_t)x.cols * 2, (uint64_t)x.cols * x.rows * 2};
-  const uint32_t b[3] = {64, mn ? 64u : (uint32_t)rows, 1};
+  const uint32_t b[3] = {mn ? 64 : tk, mn ? tk : (uint32_t)rows, (uint32_t)np};
   return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x.p, 3, d, s, b,
-                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+                   mn || tk == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
-// `value`: a result of the call (bf16: boxes of 64 columns); otherwise what a later
-// product reads (32).
-cudaError_t result_map(CUtensorMap* m, const Mat& x, bool value) {
+// Boxes of 32 rows of 64 bytes, or of 64 bf16 for a plain bf16 result (`wide`).
+cudaError_t result_map(CUtensorMap* m, const Mat& x, bool wide) {
   const uint64_t e = x.f32 ? 4 : 2;
-  const bool wide = value && !x.f32;
+  wide = wide && !x.f32;
   const uint64_t d[3] = {(uint64_t)x.cols, (uint64_t)x.rows, (uint64_t)x.planes};
   const uint64_t s[2] = {(uint64_t)x.cols * e, (uint64_t)x.cols * x.rows * e};
-  const uint32_t b[3] = {wide ? 64u : 32u, 32, 1};
+  const uint32_t b[3] = {wide ? 64u : (uint32_t)(64 / e), 32, 1};
   return make_tmap(m, x.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                    x.p, 3, d, s, b,
-                   x.f32 || wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                   wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                    CU_TENSOR_MAP_L2_PROMOTION_NONE);
-}
-
-// The segments of `pairs` products of operands with np planes each (1, or 3 with
-// the smallest of the six products first); pair i takes planes [np i, np i + np)
-// of A and map i of B.
-void segments(GemmArgs& P, int pairs, int np) {
-  P.nseg = 0;
-  for (int order = np - 1; order >= 0; --order)
-    for (int pr = 0; pr < pairs; ++pr)
-      for (int i = 0; i <= order; ++i) {
-        P.am[P.nseg] = 0;
-        P.ap[P.nseg] = (uint8_t)(np * pr + i);
-        P.bm[P.nseg] = (uint8_t)pr;
-        P.bp[P.nseg] = (uint8_t)(order - i);
-        ++P.nseg;
-      }
 }
 
 int sm_pairs() {
@@ -601,10 +617,10 @@ template <Epi E, bool AMN, bool BMN, bool F32, int TN>
 cudaError_t launch_tn(GemmArgs& P, const Opnds& o, cudaStream_t s) {
   constexpr bool DUAL = E == EPI_GATE || E == EPI_KEEP;
   using G = ftc::Cfg<TN, F32>;
-  TRY(operand_map(&P.a[0], o.a, AMN, ftc::HALF));
-  TRY(operand_map(&P.b[0], o.b[0], BMN, G::BROWS));
-  if (o.b[1].p) TRY(operand_map(&P.b[1], o.b[1], BMN, G::BROWS));
-  P.kblocks = tiles_of(o.K, ftc::TK);
+  TRY(operand_map(&P.a, o.a, AMN, ftc::HALF, G::NP));
+  TRY(operand_map(&P.b[0], o.b[0], BMN, G::BROWS, G::NP));
+  if (o.b[1].p) TRY(operand_map(&P.b[1], o.b[1], BMN, G::BROWS, G::NP));
+  P.kblocks = tiles_of(o.K, G::TK);
   P.mt = tiles_of(P.M, ftc::TM);
   P.nt = tiles_of(P.N, DUAL ? TN / 2 : TN);
   auto kern = k_ffn_tc<E, AMN, BMN, F32, TN>;
@@ -614,7 +630,7 @@ cudaError_t launch_tn(GemmArgs& P, const Opnds& o, cudaStream_t s) {
                       P);
 }
 
-// fp32: 256 x 128 tiles (three TMEM regions).  bf16: 256 x 256, or 256 x 128
+// fp32: 256 x 128 tiles (four TMEM regions).  bf16: 256 x 256, or 256 x 128
 // where its rounds over the pairs come to less: a narrow tile has half the work
 // and takes 0.72 of the time (T = 8192, C = 7168, F = 14336: 5.41 against 3.63 ms
 // for the forward pass).
@@ -653,20 +669,20 @@ GemmArgs base_args(const Ffn& f, int pairs, int64_t M, int64_t N) {
   P.act = f.act;
   P.status = f.st;
   P.wait_ns = tc::wait_limit(f.wait_ns);
-  segments(P, pairs, f.np);
+  P.nseg = pairs;
   return P;
 }
 
 // a = act(x wg^T) * (x wu^T) to a (and g, u where they are kept)
-template <bool F32> cudaError_t gate_product(const Ffn& f, void* a, void* g, void* u,
+template <bool F32> cudaError_t gate_product(const Ffn& f, void* a, float* g, float* u,
                                              cudaStream_t s) {
   GemmArgs P = base_args(f, 1, f.t, f.F);
   const Opnds o{{f.x, f.t, f.C, f.np, false},
                 {{f.wg, f.F, f.C, f.np, false}, {f.wu, f.F, f.C, f.np, false}}, f.C};
   TRY(result_map(&P.d[0], {a, f.t, f.F, f.np, false}, false));
   if (g == nullptr) return launch<EPI_GATE, false, false, F32>(P, o, s);
-  TRY(result_map(&P.d[1], {g, f.t, f.F, 1, F32}, false));
-  TRY(result_map(&P.d[2], {u, f.t, f.F, 1, F32}, false));
+  TRY(result_map(&P.d[1], {g, f.t, f.F, 1, true}, false));
+  TRY(result_map(&P.d[2], {u, f.t, f.F, 1, true}, false));
   return launch<EPI_KEEP, false, false, F32>(P, o, s);
 }
 
@@ -682,12 +698,10 @@ template <bool F32> cudaError_t fwd(const Ffn& f, void* y, void* a, cudaStream_t
       P, {{a, f.t, f.F, f.np, false}, {{f.wd, f.C, f.F, f.np, false}}, f.F}, s);
 }
 
-// a [np][t][F], d [2 np][t][F] (dg, du), g and u [t][F] in the call's type.  For
-// bf16 d may be the same memory as g and u: a tile reads its g and u before it
-// writes dg and du there.
+// a [np][t][F], d [2 np][t][F] (dg, du), g and u [t][F].
 template <bool F32>
-cudaError_t bwd(const Ffn& f, void* gx, void* gwg, void* gwu, void* gwd, void* a, void* d, void* g,
-                void* u, cudaStream_t s) {
+cudaError_t bwd(const Ffn& f, void* gx, void* gwg, void* gwu, void* gwd, void* a, void* d, float* g,
+                float* u, cudaStream_t s) {
   const int np = f.np;
   const Mat X{f.x, f.t, f.C, np, false}, GY{f.gy, f.t, f.C, np, false};
   const Mat A{a, f.t, f.F, np, false}, D{d, f.t, f.F, 2 * np, false};
@@ -731,9 +745,8 @@ cudaError_t bwd(const Ffn& f, void* gx, void* gwg, void* gwu, void* gwd, void* a
 
 size_t up(size_t v) { return (v + 255) / 256 * 256; }
 
-// Workspaces.  bf16: a; with the backward also dg and du (first g and u).
-// fp32: the split copies of the inputs, the three planes of a (and of dg, du),
-// and g, u as they are.
+// Workspaces.  The planes of a (one in bf16, three in fp32); with the backward
+// also of dg and du, and g and u in fp32.  fp32: the split copies of the inputs.
 struct Layout {
   size_t a, d, g, u, x, wg, wu, wd, gy, total;
 };
@@ -749,8 +762,8 @@ Layout layout(bool f32, bool backward, int64_t t, int64_t C, int64_t F) {
   w.a = take(hid * 2 * np);
   if (backward) {
     w.d = take(hid * 2 * 2 * np);
-    w.g = f32 ? take(hid * 4) : w.d;
-    w.u = f32 ? take(hid * 4) : w.d + hid * 2;
+    w.g = take(hid * 4);
+    w.u = take(hid * 4);
   }
   if (f32) {
     w.x = take(io * 6);
@@ -768,19 +781,20 @@ cudaError_t operands(Ffn& f, bool f32, const Layout& w, char* ws, cudaStream_t s
   f.np = f32 ? 3 : 1;
   if (!f32) return cudaSuccess;
   const int64_t io = f.t * f.C, wt = f.F * f.C;
-  TRY(split3_launch(io, f.x, ws + w.x, s));
-  TRY(split3_launch(wt, f.wg, ws + w.wg, s));
-  TRY(split3_launch(wt, f.wu, ws + w.wu, s));
-  TRY(split3_launch(wt, f.wd, ws + w.wd, s));
-  f.x = ws + w.x;
-  f.wg = ws + w.wg;
-  f.wu = ws + w.wu;
-  f.wd = ws + w.wd;
-  if (f.gy) {
-    TRY(split3_launch(io, f.gy, ws + w.gy, s));
-    f.gy = ws + w.gy;
-  }
-  return cudaSuccess;
+  SplitArgs a{};
+  auto add = [&](const void*& p, size_t off, int64_t n) {
+    a.src[a.count] = (const float*)p;
+    a.dst[a.count] = (__nv_bfloat16*)(ws + off);
+    a.n[a.count++] = n;
+    p = ws + off;
+  };
+  add(f.x, w.x, io);
+  add(f.wg, w.wg, wt);
+  add(f.wu, w.wu, wt);
+  add(f.wd, w.wd, wt);
+  if (f.gy) add(f.gy, w.gy, io);
+  const int64_t most = (std::max(io, wt) / 8 + 255) / 256;
+  return launch_after(k_split3, (unsigned)std::min<int64_t>(most, 1184), 256, 0, 1, s, a);
 }
 
 }  // namespace
@@ -813,8 +827,9 @@ cudaError_t ffn_bwd_dispatch(int dtype, int act, int64_t t, int64_t C, int64_t F
   Ffn f{t, C, F, act, 1, x, wg, wu, wd, gy, st, wait_ns};
   char* b = (char*)ws;
   TRY(operands(f, f32, w, b, s));
-  return f32 ? bwd<true>(f, gx, gwg, gwu, gwd, b + w.a, b + w.d, b + w.g, b + w.u, s)
-             : bwd<false>(f, gx, gwg, gwu, gwd, b + w.a, b + w.d, b + w.g, b + w.u, s);
+  float *g = (float*)(b + w.g), *u = (float*)(b + w.u);
+  return f32 ? bwd<true>(f, gx, gwg, gwu, gwd, b + w.a, b + w.d, g, u, s)
+             : bwd<false>(f, gx, gwg, gwu, gwd, b + w.a, b + w.d, g, u, s);
 }
 
 #undef TRY
