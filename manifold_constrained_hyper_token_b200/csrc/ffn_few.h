@@ -1,4 +1,5 @@
-// ffn_few.h -- the feed-forward products of few tokens (bf16), k_ffn_few.cu.
+// ffn_few.h -- the feed-forward products of few tokens: bf16 in k_ffn_few.cu, fp32
+// in k_ffn_few32.cu.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -25,5 +26,15 @@ cudaError_t few_down(const FewArgs& f, const void* a, void* y, cudaStream_t s);
 cudaError_t few_dgate(const FewArgs& f, const float* g, const float* u, void* d, cudaStream_t s);
 // gx = dg wg + du wu [t][C]
 cudaError_t few_grad_x(const FewArgs& f, const void* d, void* gx, cudaStream_t s);
+
+// k_ffn_few32.cu: the same in fp32, up to this many tokens.  x, gy, a and d are
+// operands in three bf16 planes each ([3][t][..], d [6][t][F]); the weights are
+// the caller's.
+constexpr int64_t kFewTokens32 = 128;
+bool few32_fits(int64_t t, int64_t C, int64_t F);
+cudaError_t few32_gate(const FewArgs& f, void* a, float* g, float* u, cudaStream_t s);
+cudaError_t few32_down(const FewArgs& f, const void* a, float* y, cudaStream_t s);
+cudaError_t few32_dgate(const FewArgs& f, const float* g, const float* u, void* d, cudaStream_t s);
+cudaError_t few32_grad_x(const FewArgs& f, const void* d, float* gx, cudaStream_t s);
 
 }  // namespace mhc

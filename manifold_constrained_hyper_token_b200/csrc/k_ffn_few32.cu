@@ -1,0 +1,502 @@
+// k_ffn_few32.cu -- the feed-forward products of up to 128 tokens, fp32.
+//
+// As in k_ffn_few.cu the weights are the tall operand and are read once, 128 rows
+// per CTA, the k axis split over a cluster.  They arrive as they are, in fp32, by
+// TMA; eight warps split each 128 x 32 tile into its three bf16 planes (split3) in
+// shared memory, and the tensor cores take six of the nine products of planes with
+// the tokens' planes (what is left out is below 2^-25 of a product).  Splitting
+// the weights beforehand, as the products of many tokens do, would move 16 bytes
+// per weight instead of 4.
+//
+// The tensor cores' adder cuts instead of rounding, so a sum is spread: the first
+// planes' products go to one of up to four accumulators in turn, by k block, the
+// other products, 2^-8 of them and less, to one of their own, and a CTA's share of
+// k is at most kMaxK per accumulator; the rest of the sum is rounded fp32 addition
+// in the epilogue.
+//
+// Warps: 0 weights' TMA, 1 the MMAs, 2 the tokens' TMA, 4-11 the split; then all
+// of them the reduction over the cluster, as in k_ffn_few.cu.
+#include "ffn_few.h"
+
+#include "ffn_common.cuh"
+#include "tc_pair.cuh"
+
+namespace mhc {
+
+namespace {
+
+namespace few32 {
+constexpr int TM = 128, TK = 32;
+constexpr int RAW = TM * TK * 4;      // a weight tile in fp32
+constexpr int PLANE = TM * TK * 2;    // ... one of its planes
+constexpr int NT = 384, NCONV = 8;    // threads; splitting warps
+constexpr int MAXRAW = 6;
+constexpr int ROOM = 222 * 1024, TAIL = 1024 + 512;
+constexpr int kMaxK = 1536;
+}  // namespace few32
+
+enum Epi32 { F32_STORE, F32_GATE, F32_DGATE };
+
+struct Few32P {
+  CUtensorMap w[2], x;
+  int nseg, kblocks;
+  int np, raws, mains;     // tokens rounded up to 16; raw stages; first-plane accumulators
+  int64_t rows, t;
+  void* o0;                // STORE: fp32 [t][rows]; else bf16 planes [3 or 6][t][rows]
+  float *g, *u;            // GATE: kept unless null; DGATE: read
+  int act;
+  uint32_t tmem_cols, npc; // columns to allocate; columns of one accumulator
+  int* status;
+  uint64_t wait_ns;
+};
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Four consecutive values as three planes, `stride` elements apart.
+__device__ __forceinline__ void store_planes(__nv_bfloat16* p, int64_t stride, const float (&v)[4]) {
+  float h[4], m[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) split3(v[i], h[i], m[i], l[i]);
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack2(h[0], h[1]), pack2(h[2], h[3]));
+  *reinterpret_cast<uint2*>(p + stride) = make_uint2(pack2(m[0], m[1]), pack2(m[2], m[3]));
+  *reinterpret_cast<uint2*>(p + 2 * stride) = make_uint2(pack2(l[0], l[1]), pack2(l[2], l[3]));
+}
+
+template <Epi32 E, bool MN>
+__global__ void __launch_bounds__(few32::NT, 1) k_ffn_few32(const __grid_constant__ Few32P P) {
+  using namespace few32;
+  constexpr int NW = E == F32_GATE ? 2 : 1;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~(uintptr_t)1023);
+  // raw stages, then two sets of [weight][plane] tiles and the tokens' planes
+  const int xbytes = 3 * P.np * TK * 2, set_bytes = NW * 3 * PLANE + xbytes;
+  uint8_t* sets = smem + P.raws * NW * RAW;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sets + 2 * set_bytes);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * MAXRAW + 7);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  auto raw_full = [&](int s) { return tc::smem_u32(bars + s); };
+  auto raw_empty = [&](int s) { return tc::smem_u32(bars + MAXRAW + s); };
+  auto set_full = [&](int s) { return tc::smem_u32(bars + 2 * MAXRAW + s); };
+  auto set_empty = [&](int s) { return tc::smem_u32(bars + 2 * MAXRAW + 2 + s); };
+  auto x_full = [&](int s) { return tc::smem_u32(bars + 2 * MAXRAW + 4 + s); };
+  const uint32_t done_bar = tc::smem_u32(bars + 2 * MAXRAW + 6);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  uint32_t csize;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
+  const int parts = (int)csize, rank = (int)tc::cluster_rank();
+  const int64_t row0 = (int64_t)(blockIdx.x / parts) * TM;
+  const int nk = P.nseg * P.kblocks;
+  // this CTA's k blocks: at least one, the launch has parts <= nk
+  const int j0 = (int)((int64_t)nk * rank / parts), j1 = (int)((int64_t)nk * (rank + 1) / parts);
+  const int blocks = j1 - j0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < P.raws; ++s) {
+      tc::mbar_init(raw_full(s), 1);
+      tc::mbar_init(raw_empty(s), NCONV);
+    }
+    for (int s = 0; s < 2; ++s) {
+      tc::mbar_init(set_full(s), NCONV);
+      tc::mbar_init(set_empty(s), 1);
+      tc::mbar_init(x_full(s), 1);
+    }
+    tc::mbar_init(done_bar, 1);
+    *abort_flag = 0;
+    tc::mbar_fence_init();
+    tc::tma_prefetch_desc(&P.w[0]);
+    tc::tma_prefetch_desc(&P.x);
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(tc::smem_u32(tmem_slot), P.tmem_cols);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  tc::grid_wait();
+  tc::grid_release();
+
+  auto give_up = [&]() {
+    *abort_flag = 1;
+    flag_status(P.status, MHC_ERR_TIMEOUT);
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------- weights, as they are
+    if (lane == 0) {
+      const uint64_t stream = tc::policy_evict_first();
+      int it = 0;
+      for (; it < blocks; ++it) {
+        const int s = it % P.raws;
+        if (it >= P.raws &&
+            !tc::mbar_pipe_wait<false>(raw_empty(s), ((uint32_t)(it / P.raws) & 1u) ^ 1u,
+                                       abort_flag, P.wait_ns)) {
+          give_up();
+          break;
+        }
+        const int j = j0 + it, seg = j / P.kblocks, k0 = (j - seg * P.kblocks) * TK;
+        tc::mbar_arrive_expect_tx(raw_full(s), NW * RAW);
+#pragma unroll
+        for (int i = 0; i < NW; ++i) {
+          const CUtensorMap* m = &P.w[NW == 2 ? i : seg];
+          const uint32_t dst = tc::smem_u32(smem + (s * NW + i) * RAW);
+          if (MN) {
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+              tc::tma_load_2d(dst + b * (RAW / 4), m, raw_full(s), (int)row0 + 32 * b, k0, stream);
+          } else {
+            tc::tma_load_2d(dst, m, raw_full(s), k0, (int)row0, stream);
+          }
+        }
+      }
+      for (int i = it > P.raws ? it - P.raws : 0; i < it; ++i)
+        tc::mbar_wait(raw_full(i % P.raws), (uint32_t)(i / P.raws) & 1u, nullptr,
+                      tc::kDrainWaitNs);
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ tokens' planes
+    if (lane == 0) {
+      const uint64_t keep = tc::policy_evict_last();
+      int it = 0;
+      for (; it < blocks; ++it) {
+        const int s = it & 1;
+        if (it >= 2 && !tc::mbar_pipe_wait<false>(set_empty(s), ((uint32_t)(it / 2) & 1u) ^ 1u,
+                                                  abort_flag, P.wait_ns)) {
+          give_up();
+          break;
+        }
+        const int j = j0 + it, seg = j / P.kblocks, k0 = (j - seg * P.kblocks) * TK;
+        tc::mbar_arrive_expect_tx(x_full(s), xbytes);
+        tc::tma_load_3d(tc::smem_u32(sets + s * set_bytes + NW * 3 * PLANE), &P.x, x_full(s), k0,
+                        0, NW == 2 ? 0 : 3 * seg, keep);
+      }
+      for (int i = it > 2 ? it - 2 : 0; i < it; ++i)
+        tc::mbar_wait(x_full(i & 1), (uint32_t)(i / 2) & 1u, nullptr, tc::kDrainWaitNs);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------------- MMA
+    if (lane == 0) {
+      const uint32_t idesc = tc::idesc_bf16(TM, P.np, MN, false);
+      for (int it = 0; it < blocks; ++it) {
+        const int s = it & 1;
+        const uint32_t par = (uint32_t)(it / 2) & 1u;
+        if (!tc::mbar_pipe_wait<false>(set_full(s), par, abort_flag, P.wait_ns) ||
+            !tc::mbar_pipe_wait<false>(x_full(s), par, abort_flag, P.wait_ns)) {
+          give_up();
+          break;
+        }
+        tc::tc_fence_after();
+        const uint32_t base = tc::smem_u32(sets + s * set_bytes);
+        const int main = it % P.mains;
+#pragma unroll
+        for (int i = 0; i < NW; ++i) {
+          const uint32_t acc = tmem + i * (1 + P.mains) * P.npc;
+          auto mma = [&](uint32_t col, int pw, int px, int k, bool add) {
+            const uint32_t wb = base + (i * 3 + pw) * PLANE;
+            const uint64_t a = MN ? tc::smem_desc(wb + k * 2048, PLANE / 2, 1024, tc::SWZ_128B)
+                                  : tc::smem_desc(wb + k * 32, 16, 512, tc::SWZ_64B);
+            const uint64_t b = tc::smem_desc(base + NW * 3 * PLANE + px * P.np * 64 + k * 32, 16,
+                                             512, tc::SWZ_64B);
+            tc::mma_bf16(col, a, b, idesc, add ? 1u : 0u);
+          };
+#pragma unroll
+          for (int k = 0; k < TK / 16; ++k) {
+            mma(acc, 2, 0, k, it > 0 || k > 0);
+            mma(acc, 1, 1, k, true);
+            mma(acc, 0, 2, k, true);
+            mma(acc, 1, 0, k, true);
+            mma(acc, 0, 1, k, true);
+            mma(acc + (1 + main) * P.npc, 0, 0, k, it >= P.mains || k > 0);
+          }
+        }
+        tc::mma_commit(set_empty(s));
+      }
+      // the sums are complete, and no MMA is under way when TMEM is freed
+      tc::mma_commit(done_bar);
+      tc::mbar_wait(done_bar, 0, nullptr, tc::kDrainWaitNs);
+    }
+  } else if (warp >= 4) {
+    // -------------------------------------------------------------------- split
+    const int c = threadIdx.x - 128;
+    for (int it = 0; it < blocks; ++it) {
+      const int rs = it % P.raws, s = it & 1;
+      bool ok = tc::mbar_pipe_wait<false>(raw_full(rs), (uint32_t)(it / P.raws) & 1u, abort_flag,
+                                          P.wait_ns);
+      if (ok && it >= 2)
+        ok = tc::mbar_pipe_wait<false>(set_empty(s), ((uint32_t)(it / 2) & 1u) ^ 1u, abort_flag,
+                                       P.wait_ns);
+      if (!ok && !*abort_flag) give_up();
+      if (!__all_sync(0xffffffffu, ok)) break;  // a warp leaves as one
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        const uint8_t* src = smem + (rs * NW + i) * RAW;
+        uint8_t* dst = sets + s * set_bytes + i * 3 * PLANE;
+#pragma unroll
+        for (int e = 0; e < RAW / 16 / (32 * NCONV); ++e) {
+          // 16 bytes of the tile: row r of 128 bytes, piece p
+          const int at = c + e * 32 * NCONV, r = at >> 3, p = at & 7;
+          const float4 v = *reinterpret_cast<const float4*>(src + at * 16);
+          float h[4], m[4], l[4];
+          split3(v.x, h[0], m[0], l[0]);
+          split3(v.y, h[1], m[1], l[1]);
+          split3(v.z, h[2], m[2], l[2]);
+          split3(v.w, h[3], m[3], l[3]);
+          int to;
+          if (MN) {
+            // tile [32 rows of W at a time][k][32]: r = 32 block + k
+            const int blk = r >> 5, k = r & 31;
+            to = (blk >> 1) * (PLANE / 2) + k * 128 +
+                 ((((blk & 1) * 4 + (p >> 1)) ^ (k & 7)) << 4) + (p & 1) * 8;
+          } else {
+            to = r * 64 + (((p >> 1) ^ ((r >> 1) & 3)) << 4) + (p & 1) * 8;
+          }
+          *reinterpret_cast<uint2*>(dst + to) = make_uint2(pack2(h[0], h[1]), pack2(h[2], h[3]));
+          *reinterpret_cast<uint2*>(dst + PLANE + to) =
+              make_uint2(pack2(m[0], m[1]), pack2(m[2], m[3]));
+          *reinterpret_cast<uint2*>(dst + 2 * PLANE + to) =
+              make_uint2(pack2(l[0], l[1]), pack2(l[2], l[3]));
+        }
+      }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_arrive(set_full(s));
+        tc::mbar_arrive(raw_empty(rs));
+      }
+    }
+  }
+  __syncthreads();
+  tc::tc_fence_after();
+  // This CTA's part, [weight][token][row], over the stages, whose copies and MMAs
+  // are done; then the ranks add up the tokens in turn, parts in rank order.
+  float* part = reinterpret_cast<float*>(smem);
+  if (warp < 4) {
+    const int r = threadIdx.x;
+    const uint32_t ta = tmem + ((uint32_t)(32 * warp) << 16);
+    const int used = blocks < P.mains ? blocks : P.mains;
+#pragma unroll
+    for (int i = 0; i < NW; ++i)
+      for (int c = 0; c < P.np; c += 16) {
+        float v[16], m[16];
+        const uint32_t acc = ta + i * (1 + P.mains) * P.npc + c;
+        tc::tmem_get16(acc, v);
+        for (int q = 0; q < used; ++q) {
+          tc::tmem_get16(acc + (1 + q) * P.npc, m);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] += m[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) part[(i * P.np + c + e) * TM + r] = v[e];
+      }
+  }
+  __syncwarp();
+  if (parts > 1) tc::cluster_sync();
+  else __syncthreads();
+  const int64_t row = row0 + 4 * lane, plane = P.t * P.rows;
+  if (row < P.rows) {
+    for (int64_t c = rank + parts * warp; c < P.t; c += parts * (NT / 32)) {
+      const int64_t o = c * P.rows + row;
+      float4 gq, uq;
+      if (E == F32_DGATE) {
+        gq = *reinterpret_cast<const float4*>(P.g + o);
+        uq = *reinterpret_cast<const float4*>(P.u + o);
+      }
+      float4 ld[NW][8];
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        const uint32_t at = tc::smem_u32(part + (i * P.np + c) * TM + 4 * lane);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          ld[i][q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (q < parts) ld[i][q] = tc::ld_cluster_f32x4(tc::map_cta(at, q));
+        }
+      }
+      float v[NW][4];
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          v[i][0] += ld[i][q].x;
+          v[i][1] += ld[i][q].y;
+          v[i][2] += ld[i][q].z;
+          v[i][3] += ld[i][q].w;
+        }
+      }
+      if (E == F32_STORE) {
+        *reinterpret_cast<float4*>((float*)P.o0 + o) = make_float4(v[0][0], v[0][1], v[0][2],
+                                                                   v[0][3]);
+      } else if (E == F32_GATE) {
+        float a[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) a[k] = gate<false>(P.act, v[0][k]) * v[NW - 1][k];
+        store_planes((__nv_bfloat16*)P.o0 + o, plane, a);
+        if (P.g) {
+          *reinterpret_cast<float4*>(P.g + o) = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
+          *reinterpret_cast<float4*>(P.u + o) =
+              make_float4(v[NW - 1][0], v[NW - 1][1], v[NW - 1][2], v[NW - 1][3]);
+        }
+      } else {
+        const float g[4] = {gq.x, gq.y, gq.z, gq.w}, u[4] = {uq.x, uq.y, uq.z, uq.w};
+        float dg[4], du[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float h, dh;
+          gate_both<false>(P.act, g[k], h, dh);
+          dg[k] = v[0][k] * u[k] * dh;
+          du[k] = v[0][k] * h;
+        }
+        store_planes((__nv_bfloat16*)P.o0 + o, plane, dg);
+        store_planes((__nv_bfloat16*)P.o0 + 3 * plane + o, plane, du);
+      }
+    }
+  }
+  tc::tc_fence_before();
+  __syncwarp();
+  // nobody reads this CTA's part any more
+  if (parts > 1) tc::cluster_sync();
+  else __syncthreads();
+  if (warp == 1) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, P.tmem_cols);
+  }
+}
+
+#define TRY(call)                         \
+  do {                                    \
+    const cudaError_t e_ = (call);        \
+    if (e_ != cudaSuccess) return e_;     \
+  } while (0)
+
+// An fp32 weight [rows][cols] as stored; mn: the products' rows run along cols.
+cudaError_t weight_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, bool mn) {
+  const uint64_t d[2] = {(uint64_t)cols, (uint64_t)rows};
+  const uint64_t s[1] = {(uint64_t)cols * 4};
+  const uint32_t b[2] = {32, mn ? (uint32_t)few32::TK : (uint32_t)few32::TM};
+  return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p, 2, d, s, b, CU_TENSOR_MAP_SWIZZLE_NONE,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+// The tokens' planes [planes][t][K], three at a time
+cudaError_t token_map(CUtensorMap* m, const void* p, int64_t t, int64_t K, int planes, int np) {
+  const uint64_t d[3] = {(uint64_t)K, (uint64_t)t, (uint64_t)planes};
+  const uint64_t s[2] = {(uint64_t)K * 2, (uint64_t)K * t * 2};
+  const uint32_t b[3] = {few32::TK, (uint32_t)np, 3};
+  return make_tmap_bf16(m, p, 3, d, s, b, CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+    return 148;
+  return n;
+}
+
+int tokens16(int64_t t) { return (int)((t + 15) / 16 * 16); }
+
+// First-plane accumulators of a product with nw weights: what TMEM holds beside
+// the one of the other planes, up to four.
+int mains_of(int64_t t, int nw) {
+  const int npc = (tokens16(t) + 31) / 32 * 32, n = 512 / (nw * npc) - 1;
+  return n < 4 ? n : 4;
+}
+
+template <Epi32 E, bool MN>
+cudaError_t launch(Few32P& P, const FewArgs& f, int64_t K, cudaStream_t s) {
+  using namespace few32;
+  constexpr int NW = E == F32_GATE ? 2 : 1;
+  P.t = f.t;
+  P.act = f.act;
+  P.status = f.st;
+  P.wait_ns = tc::wait_limit(f.wait_ns);
+  P.kblocks = (int)((K + TK - 1) / TK);
+  P.npc = (uint32_t)((P.np + 31) / 32 * 32);
+  P.mains = mains_of(f.t, NW);
+  P.tmem_cols = 32;
+  while (P.tmem_cols < NW * (1 + P.mains) * P.npc) P.tmem_cols *= 2;
+  const int sets = 2 * (NW * 3 * PLANE + 3 * P.np * TK * 2);
+  P.raws = (ROOM - sets) / (NW * RAW);
+  if (P.raws > MAXRAW) P.raws = MAXRAW;
+  // the parts take the stages' place: NW np 512 bytes, less than the two sets
+  const int stage = sets + P.raws * NW * RAW;
+  const int64_t tiles = (P.rows + TM - 1) / TM, slots = sm_count();
+  const int nk = P.nseg * P.kblocks;
+  int parts = 0;
+  int64_t best = 0;
+  for (int p = 1; p <= 8 && p <= nk; p *= 2) {
+    if ((int64_t)(nk + p - 1) / p * TK > (int64_t)kMaxK * P.mains && p < 8 && 2 * p <= nk)
+      continue;
+    const int64_t cost = ((tiles * p + slots - 1) / slots) * ((nk + p - 1) / p + 6);
+    if (parts == 0 || cost < best) {
+      best = cost;
+      parts = p;
+    }
+  }
+  auto kern = k_ffn_few32<E, MN>;
+  const int smem = stage + TAIL;
+  TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  return launch_after(kern, (unsigned)(tiles * parts), NT, smem, (unsigned)parts, s, P);
+}
+
+Few32P base(const FewArgs& f, int64_t rows, int nseg) {
+  Few32P P{};
+  P.rows = rows;
+  P.nseg = nseg;
+  P.np = tokens16(f.t);
+  return P;
+}
+
+}  // namespace
+
+bool few32_fits(int64_t t, int64_t C, int64_t F) {
+  if (t > kFewTokens32) return false;
+  const int64_t one = (int64_t)8 * few32::kMaxK;
+  return C <= one * mains_of(t, 2) && 2 * F <= one * mains_of(t, 1);
+}
+
+cudaError_t few32_gate(const FewArgs& f, void* a, float* g, float* u, cudaStream_t s) {
+  Few32P P = base(f, f.F, 1);
+  TRY(weight_map(&P.w[0], f.wg, f.F, f.C, false));
+  TRY(weight_map(&P.w[1], f.wu, f.F, f.C, false));
+  TRY(token_map(&P.x, f.x, f.t, f.C, 3, P.np));
+  P.o0 = a;
+  P.g = g;
+  P.u = u;
+  return launch<F32_GATE, false>(P, f, f.C, s);
+}
+
+cudaError_t few32_down(const FewArgs& f, const void* a, float* y, cudaStream_t s) {
+  Few32P P = base(f, f.C, 1);
+  TRY(weight_map(&P.w[0], f.wd, f.C, f.F, false));
+  TRY(token_map(&P.x, a, f.t, f.F, 3, P.np));
+  P.o0 = y;
+  return launch<F32_STORE, false>(P, f, f.F, s);
+}
+
+cudaError_t few32_dgate(const FewArgs& f, const float* g, const float* u, void* d, cudaStream_t s) {
+  Few32P P = base(f, f.F, 1);
+  TRY(weight_map(&P.w[0], f.wd, f.C, f.F, true));
+  TRY(token_map(&P.x, f.gy, f.t, f.C, 3, P.np));
+  P.o0 = d;
+  P.g = const_cast<float*>(g);
+  P.u = const_cast<float*>(u);
+  return launch<F32_DGATE, true>(P, f, f.C, s);
+}
+
+cudaError_t few32_grad_x(const FewArgs& f, const void* d, float* gx, cudaStream_t s) {
+  Few32P P = base(f, f.C, 2);
+  TRY(weight_map(&P.w[0], f.wg, f.F, f.C, true));
+  TRY(weight_map(&P.w[1], f.wu, f.F, f.C, true));
+  TRY(token_map(&P.x, d, f.t, f.F, 6, P.np));
+  P.o0 = gx;
+  return launch<F32_STORE, true>(P, f, f.F, s);
+}
+
+#undef TRY
+
+}  // namespace mhc

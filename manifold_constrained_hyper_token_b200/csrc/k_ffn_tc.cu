@@ -657,6 +657,7 @@ struct Ffn {
   const void *x, *wg, *wu, *wd, *gy;
   int* st;
   int64_t wait_ns;
+  bool is_few() const { return np == 3 ? few32_fits(t, C, F) : t <= kFewTokens; }
   FewArgs few() const { return {t, C, F, act, x, wg, wu, wd, gy, st, wait_ns}; }
 };
 
@@ -687,9 +688,14 @@ template <bool F32> cudaError_t gate_product(const Ffn& f, void* a, float* g, fl
 }
 
 template <bool F32> cudaError_t fwd(const Ffn& f, void* y, void* a, cudaStream_t s) {
-  if (!F32 && f.t <= kFewTokens) {
-    TRY(few_gate(f.few(), a, nullptr, nullptr, s));
-    return few_down(f.few(), a, y, s);
+  if (f.is_few()) {
+    if constexpr (F32) {
+      TRY(few32_gate(f.few(), a, nullptr, nullptr, s));
+      return few32_down(f.few(), a, (float*)y, s);
+    } else {
+      TRY(few_gate(f.few(), a, nullptr, nullptr, s));
+      return few_down(f.few(), a, y, s);
+    }
   }
   TRY(gate_product<F32>(f, a, nullptr, nullptr, s));
   GemmArgs P = base_args(f, 1, f.t, f.C);
@@ -707,8 +713,11 @@ cudaError_t bwd(const Ffn& f, void* gx, void* gwg, void* gwu, void* gwd, void* a
   const Mat A{a, f.t, f.F, np, false}, D{d, f.t, f.F, 2 * np, false};
   const Mat WG{f.wg, f.F, f.C, np, false}, WU{f.wu, f.F, f.C, np, false};
   const Mat WD{f.wd, f.C, f.F, np, false};
-  const bool few = !F32 && f.t <= kFewTokens;
-  if (few) {
+  const bool few = f.is_few();
+  if (few && F32) {
+    TRY(few32_gate(f.few(), a, g, u, s));
+    TRY(few32_dgate(f.few(), g, u, d, s));
+  } else if (few) {
     TRY(few_gate(f.few(), a, g, u, s));
     TRY(few_dgate(f.few(), g, u, d, s));
   } else {
@@ -721,7 +730,9 @@ cudaError_t bwd(const Ffn& f, void* gx, void* gwg, void* gwu, void* gwd, void* a
   }
   // the rest needs only what is finished when the next kernel starts: the three
   // run beside one another, each filling the SMs that the one before leaves idle
-  if (few) {
+  if (few && F32) {
+    TRY(few32_grad_x(f.few(), d, (float*)gx, s));
+  } else if (few) {
     TRY(few_grad_x(f.few(), d, gx, s));
   } else {
     GemmArgs P = base_args(f, 2, f.t, f.C);
@@ -746,7 +757,8 @@ cudaError_t bwd(const Ffn& f, void* gx, void* gwg, void* gwu, void* gwd, void* a
 size_t up(size_t v) { return (v + 255) / 256 * 256; }
 
 // Workspaces.  The planes of a (one in bf16, three in fp32); with the backward
-// also of dg and du, and g and u in fp32.  fp32: the split copies of the inputs.
+// also of dg and du, and g and u in fp32.  fp32: the split copies of the inputs
+// (with few tokens the weights are split on their way into the products).
 struct Layout {
   size_t a, d, g, u, x, wg, wu, wd, gy, total;
 };
@@ -767,10 +779,12 @@ Layout layout(bool f32, bool backward, int64_t t, int64_t C, int64_t F) {
   }
   if (f32) {
     w.x = take(io * 6);
-    w.wg = take(wt * 6);
-    w.wu = take(wt * 6);
-    w.wd = take(wt * 6);
     if (backward) w.gy = take(io * 6);
+    if (!few32_fits(t, C, F)) {
+      w.wg = take(wt * 6);
+      w.wu = take(wt * 6);
+      w.wd = take(wt * 6);
+    }
   }
   w.total = off;
   return w;
@@ -789,11 +803,13 @@ cudaError_t operands(Ffn& f, bool f32, const Layout& w, char* ws, cudaStream_t s
     p = ws + off;
   };
   add(f.x, w.x, io);
-  add(f.wg, w.wg, wt);
-  add(f.wu, w.wu, wt);
-  add(f.wd, w.wd, wt);
   if (f.gy) add(f.gy, w.gy, io);
-  const int64_t most = (std::max(io, wt) / 8 + 255) / 256;
+  if (!f.is_few()) {
+    add(f.wg, w.wg, wt);
+    add(f.wu, w.wu, wt);
+    add(f.wd, w.wd, wt);
+  }
+  const int64_t most = ((f.is_few() ? io : std::max(io, wt)) / 8 + 255) / 256;
   return launch_after(k_split3, (unsigned)std::min<int64_t>(most, 1184), 256, 0, 1, s, a);
 }
 
