@@ -2,7 +2,7 @@
 //
 // As in k_ffn_few.cu the weights are the tall operand and are read once, 128 rows
 // per CTA, the k axis split over a cluster.  They arrive as they are, in fp32, by
-// TMA; eight warps split each 128 x 32 tile into its three bf16 planes (split3) in
+// TMA; eight warps split each 128 x 32 tile into its three bf16 planes (split3x4) in
 // shared memory, and the tensor cores take six of the nine products of planes with
 // the tokens' planes (what is left out is below 2^-25 of a product).  Splitting
 // the weights beforehand, as the products of many tokens do, would move 16 bytes
@@ -14,7 +14,8 @@
 // k is at most kMaxK per accumulator; the rest of the sum is rounded fp32 addition
 // in the epilogue.
 //
-// Warps: 0 weights' TMA, 1 the MMAs, 2 the tokens' TMA, 4-11 the split; then all
+// Warps: 0 weights' TMA, 1 the MMAs, 2 the tokens' TMA, 4-11 and 12-19 the split of
+// the even and of the odd k blocks, each with a set of planes of its own; then all
 // of them the reduction over the cluster, as in k_ffn_few.cu.
 #include "ffn_few.h"
 
@@ -29,7 +30,7 @@ namespace few32 {
 constexpr int TM = 128, TK = 32;
 constexpr int RAW = TM * TK * 4;      // a weight tile in fp32
 constexpr int PLANE = TM * TK * 2;    // ... one of its planes
-constexpr int NT = 384, NCONV = 8;    // threads; splitting warps
+constexpr int NT = 640, NCONV = 8;    // threads; splitting warps of a set of planes
 constexpr int MAXRAW = 6;
 constexpr int ROOM = 222 * 1024, TAIL = 1024 + 512;
 constexpr int kMaxK = 1536;
@@ -50,18 +51,13 @@ struct Few32P {
   uint64_t wait_ns;
 };
 
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 // Four consecutive values as three planes, `stride` elements apart.
 __device__ __forceinline__ void store_planes(__nv_bfloat16* p, int64_t stride, const float (&v)[4]) {
-  float h[4], m[4], l[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) split3(v[i], h[i], m[i], l[i]);
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack2(h[0], h[1]), pack2(h[2], h[3]));
-  *reinterpret_cast<uint2*>(p + stride) = make_uint2(pack2(m[0], m[1]), pack2(m[2], m[3]));
-  *reinterpret_cast<uint2*>(p + 2 * stride) = make_uint2(pack2(l[0], l[1]), pack2(l[2], l[3]));
+  uint2 h, m, l;
+  split3x4(make_float4(v[0], v[1], v[2], v[3]), h, m, l);
+  *reinterpret_cast<uint2*>(p) = h;
+  *reinterpret_cast<uint2*>(p + stride) = m;
+  *reinterpret_cast<uint2*>(p + 2 * stride) = l;
 }
 
 template <Epi32 E, bool MN>
@@ -222,8 +218,8 @@ __global__ void __launch_bounds__(few32::NT, 1) k_ffn_few32(const __grid_constan
     }
   } else if (warp >= 4) {
     // -------------------------------------------------------------------- split
-    const int c = threadIdx.x - 128;
-    for (int it = 0; it < blocks; ++it) {
+    const int c = (threadIdx.x - 128) % (32 * NCONV);
+    for (int it = (warp - 4) / NCONV; it < blocks; it += 2) {
       const int rs = it % P.raws, s = it & 1;
       bool ok = tc::mbar_pipe_wait<false>(raw_full(rs), (uint32_t)(it / P.raws) & 1u, abort_flag,
                                           P.wait_ns);
@@ -241,11 +237,8 @@ __global__ void __launch_bounds__(few32::NT, 1) k_ffn_few32(const __grid_constan
           // 16 bytes of the tile: row r of 128 bytes, piece p
           const int at = c + e * 32 * NCONV, r = at >> 3, p = at & 7;
           const float4 v = *reinterpret_cast<const float4*>(src + at * 16);
-          float h[4], m[4], l[4];
-          split3(v.x, h[0], m[0], l[0]);
-          split3(v.y, h[1], m[1], l[1]);
-          split3(v.z, h[2], m[2], l[2]);
-          split3(v.w, h[3], m[3], l[3]);
+          uint2 h, m, l;
+          split3x4(v, h, m, l);
           int to;
           if (MN) {
             // tile [32 rows of W at a time][k][32]: r = 32 block + k
@@ -255,11 +248,9 @@ __global__ void __launch_bounds__(few32::NT, 1) k_ffn_few32(const __grid_constan
           } else {
             to = r * 64 + (((p >> 1) ^ ((r >> 1) & 3)) << 4) + (p & 1) * 8;
           }
-          *reinterpret_cast<uint2*>(dst + to) = make_uint2(pack2(h[0], h[1]), pack2(h[2], h[3]));
-          *reinterpret_cast<uint2*>(dst + PLANE + to) =
-              make_uint2(pack2(m[0], m[1]), pack2(m[2], m[3]));
-          *reinterpret_cast<uint2*>(dst + 2 * PLANE + to) =
-              make_uint2(pack2(l[0], l[1]), pack2(l[2], l[3]));
+          *reinterpret_cast<uint2*>(dst + to) = h;
+          *reinterpret_cast<uint2*>(dst + PLANE + to) = m;
+          *reinterpret_cast<uint2*>(dst + 2 * PLANE + to) = l;
         }
       }
       tc::fence_proxy_async_smem();

@@ -18,7 +18,7 @@
 // Tiles go over the pairs in bands of eight row tiles, so that the tiles in
 // flight share operands in L2.
 //
-// fp32 operands come as three bf16 planes each (their exact split, split3).  A
+// fp32 operands come as three bf16 planes each (their exact split, split3x4).  A
 // stage brings all planes of a 32-wide k block and six of the nine products of
 // planes are taken, those whose orders add up to at most two; what is left out is
 // below 2^-25 of a product.  The tensor cores' adder cuts instead of rounding,
@@ -135,11 +135,6 @@ __device__ __forceinline__ uint64_t rows_desc(uint32_t base, int plane, int k) {
                        G::TK == 64 ? tc::SWZ_128B : tc::SWZ_64B);
 }
 
-__device__ __forceinline__ uint32_t bf2(float a, float b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 // Row `lane` of a staged box (64-byte rows with the 64-byte swizzle): columns
 // [16 g, 16 g + 16) of 32 bf16, or 16 fp32.
 __device__ __forceinline__ uint4* box_piece(uint8_t* box, int lane, int p) {
@@ -166,12 +161,18 @@ __device__ __forceinline__ void put_operand(uint8_t* box, int lane, int g, const
   if (!F32) {
     put_bf16(box, lane, g, v);
   } else {
-    float h[16], m[16], l[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) split3(v[i], h[i], m[i], l[i]);
-    put_bf16(box, lane, g, h);
-    put_bf16(box + ftc::BOX, lane, g, m);
-    put_bf16(box + 2 * ftc::BOX, lane, g, l);
+    for (int p = 0; p < 2; ++p) {
+      uint2 h[2], m[2], l[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int i = 8 * p + 4 * e;
+        split3x4(make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]), h[e], m[e], l[e]);
+      }
+      *box_piece(box, lane, 2 * g + p) = make_uint4(h[0].x, h[0].y, h[1].x, h[1].y);
+      *box_piece(box + ftc::BOX, lane, 2 * g + p) = make_uint4(m[0].x, m[0].y, m[1].x, m[1].y);
+      *box_piece(box + 2 * ftc::BOX, lane, 2 * g + p) = make_uint4(l[0].x, l[0].y, l[1].x, l[1].y);
+    }
   }
 }
 
@@ -544,17 +545,15 @@ __global__ void __launch_bounds__(256) k_split3(const __grid_constant__ SplitArg
     const int64_t n = a.n[q];
     for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n;
          i += (int64_t)gridDim.x * 256 * 8) {
-      float p[3][8];
+      uint2 p[3][2];
 #pragma unroll
-      for (int h = 0; h < 8; h += 4) {
-        const float4 f = __ldcs(reinterpret_cast<const float4*>(a.src[q] + i + h));
-        const float w[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) split3(w[e], p[0][h + e], p[1][h + e], p[2][h + e]);
-      }
+      for (int h = 0; h < 2; ++h)
+        split3x4(__ldcs(reinterpret_cast<const float4*>(a.src[q] + i + 4 * h)), p[0][h], p[1][h],
+                 p[2][h]);
 #pragma unroll
       for (int pl = 0; pl < 3; ++pl)
-        *reinterpret_cast<uint4*>(a.dst[q] + pl * n + i) = Vec<__nv_bfloat16>::pack(p[pl]);
+        *reinterpret_cast<uint4*>(a.dst[q] + pl * n + i) =
+            make_uint4(p[pl][0].x, p[pl][0].y, p[pl][1].x, p[pl][1].y);
     }
   }
 }
