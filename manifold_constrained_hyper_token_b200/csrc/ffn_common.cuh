@@ -29,35 +29,30 @@ template <bool FAST> __device__ __forceinline__ float gate(int act, float g) {
   return g * (0.5f * erfcf(-0.70710678118654752f * g));
 }
 
-// bf16 pairs: two floats rounded to one register, and back.
+// Two floats rounded to a bf16 pair.
 __device__ __forceinline__ uint32_t bf2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// v = hi + mid + lo exactly (8 bits each; lo may lose what lies below bf16's
-// smallest value): the residual after each rounding to bf16 is an fp32 number.
-// Four values, packed in order.  A finite value whose rounding would reach
-// infinity is cut instead, and an infinity has no residual; both are rare and
-// looked for four at a time.
+// v = hi + mid + lo exactly, three bf16 numbers of 8 bits each (lo may lose what
+// lies below bf16's smallest value).  The upper half of an fp32 number is the
+// bf16 number it is cut to, so each plane is a mask and a subtraction; cutting
+// rather than rounding leaves mid below 2^-7 of v and lo below 2^-15, and cannot
+// overflow.  Non-finite values stay non-finite.  Four values, packed in order.
 __device__ __forceinline__ void split3x4(const float4 v, uint2& hi, uint2& mid, uint2& lo) {
-  constexpr float kLast = 3.38e38f;  // below bf16's largest value, 3.3895e38
-  hi = make_uint2(bf2(v.x, v.y), bf2(v.z, v.w));
-  if (fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))) > kLast)
-    hi = make_uint2(__float_as_uint(v.x) >> 16 | (__float_as_uint(v.y) & 0xffff0000u),
-                    __float_as_uint(v.z) >> 16 | (__float_as_uint(v.w) & 0xffff0000u));
-  float r[4] = {v.x - bf_lo(hi.x), v.y - bf_hi(hi.x), v.z - bf_lo(hi.y), v.w - bf_hi(hi.y)};
-  if (fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))) > kLast) {
-    if (isinf(v.x)) r[0] = 0.0f;
-    if (isinf(v.y)) r[1] = 0.0f;
-    if (isinf(v.z)) r[2] = 0.0f;
-    if (isinf(v.w)) r[3] = 0.0f;
+  const float in[4] = {v.x, v.y, v.z, v.w};
+  uint32_t h[4], m[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h[i] = __float_as_uint(in[i]);
+    const float r = in[i] - __uint_as_float(h[i] & 0xffff0000u);
+    m[i] = __float_as_uint(r);
+    l[i] = __float_as_uint(r - __uint_as_float(m[i] & 0xffff0000u));
   }
-  mid = make_uint2(bf2(r[0], r[1]), bf2(r[2], r[3]));
-  lo = make_uint2(bf2(r[0] - bf_lo(mid.x), r[1] - bf_hi(mid.x)),
-                  bf2(r[2] - bf_lo(mid.y), r[3] - bf_hi(mid.y)));
+  hi = make_uint2(__byte_perm(h[0], h[1], 0x7632), __byte_perm(h[2], h[3], 0x7632));
+  mid = make_uint2(__byte_perm(m[0], m[1], 0x7632), __byte_perm(m[2], m[3], 0x7632));
+  lo = make_uint2(__byte_perm(l[0], l[1], 0x7632), __byte_perm(l[2], l[3], 0x7632));
 }
 
 }  // namespace mhc

@@ -2,17 +2,22 @@
 //
 // As in k_ffn_few.cu the weights are the tall operand and are read once, 128 rows
 // per CTA, the k axis split over a cluster.  They arrive as they are, in fp32, by
-// TMA; eight warps split each 128 x 32 tile into its three bf16 planes (split3x4) in
+// TMA; two groups of eight warps split each 128 x 32 tile into its three bf16 planes (split3x4) in
 // shared memory, and the tensor cores take six of the nine products of planes with
-// the tokens' planes (what is left out is below 2^-25 of a product).  Splitting
+// the tokens' planes (what is left out is 2^-24 of a product on average).  Splitting
 // the weights beforehand, as the products of many tokens do, would move 16 bytes
 // per weight instead of 4.
 //
-// The tensor cores' adder cuts instead of rounding, so a sum is spread: the first
-// planes' products go to one of up to four accumulators in turn, by k block, the
-// other products, 2^-8 of them and less, to one of their own, and a CTA's share of
-// k is at most kMaxK per accumulator; the rest of the sum is rounded fp32 addition
-// in the epilogue.
+// A small MMA takes about as long as one of N = 128, so the tokens' planes lie one
+// after the other as one operand of 3 np rows, and three MMAs per 16 k do for six:
+//   W1 [X1 X2 X3] -> [D0 D1 D2],  W2 [X1 X2] -> [D1 D2],  W3 [X1] -> [D2]
+// with one accumulator D_o per order o (T = 1, C = 7168, F = 14336: 540 us with six).
+// Beyond 80 tokens N and TMEM do not hold that; there the six go to two
+// accumulators, orders 1 and 2 together.
+//
+// The tensor cores' adder cuts instead of rounding, so a long sum is spread over up
+// to four sets of accumulators in turn, and a CTA's share of k is at most kMaxK per
+// set; the rest of the sum is rounded fp32 addition in the epilogue.
 //
 // Warps: 0 weights' TMA, 1 the MMAs, 2 the tokens' TMA, 4-11 and 12-19 the split of
 // the even and of the odd k blocks, each with a set of planes of its own; then all
@@ -33,7 +38,8 @@ constexpr int PLANE = TM * TK * 2;    // ... one of its planes
 constexpr int NT = 640, NCONV = 8;    // threads; splitting warps of a set of planes
 constexpr int MAXRAW = 6;
 constexpr int ROOM = 222 * 1024, TAIL = 1024 + 512;
-constexpr int kMaxK = 1536;
+constexpr int kMaxK = 2048;
+static_assert(RAW / 4 == 32 * NCONV * 16, "a thread takes 16 bytes of each quarter of a tile");
 }  // namespace few32
 
 enum Epi32 { F32_STORE, F32_GATE, F32_DGATE };
@@ -41,12 +47,13 @@ enum Epi32 { F32_STORE, F32_GATE, F32_DGATE };
 struct Few32P {
   CUtensorMap w[2], x;
   int nseg, kblocks;
-  int np, raws, mains;     // tokens rounded up to 16; raw stages; first-plane accumulators
+  int np, raws;            // tokens rounded up to 16; raw stages
+  int sets, orders;        // accumulator sets of a weight; accumulators in a set (3, or 2)
   int64_t rows, t;
   void* o0;                // STORE: fp32 [t][rows]; else bf16 planes [3 or 6][t][rows]
   float *g, *u;            // GATE: kept unless null; DGATE: read
   int act;
-  uint32_t tmem_cols, npc; // columns to allocate; columns of one accumulator
+  uint32_t tmem_cols;      // columns to allocate; an accumulator has np
   int* status;
   uint64_t wait_ns;
 };
@@ -177,7 +184,6 @@ __global__ void __launch_bounds__(few32::NT, 1) k_ffn_few32(const __grid_constan
   } else if (warp == 1) {
     // ---------------------------------------------------------------------- MMA
     if (lane == 0) {
-      const uint32_t idesc = tc::idesc_bf16(TM, P.np, MN, false);
       for (int it = 0; it < blocks; ++it) {
         const int s = it & 1;
         const uint32_t par = (uint32_t)(it / 2) & 1u;
@@ -188,26 +194,32 @@ __global__ void __launch_bounds__(few32::NT, 1) k_ffn_few32(const __grid_constan
         }
         tc::tc_fence_after();
         const uint32_t base = tc::smem_u32(sets + s * set_bytes);
-        const int main = it % P.mains;
 #pragma unroll
-        for (int i = 0; i < NW; ++i) {
-          const uint32_t acc = tmem + i * (1 + P.mains) * P.npc;
-          auto mma = [&](uint32_t col, int pw, int px, int k, bool add) {
-            const uint32_t wb = base + (i * 3 + pw) * PLANE;
-            const uint64_t a = MN ? tc::smem_desc(wb + k * 2048, PLANE / 2, 1024, tc::SWZ_128B)
-                                  : tc::smem_desc(wb + k * 32, 16, 512, tc::SWZ_64B);
-            const uint64_t b = tc::smem_desc(base + NW * 3 * PLANE + px * P.np * 64 + k * 32, 16,
-                                             512, tc::SWZ_64B);
-            tc::mma_bf16(col, a, b, idesc, add ? 1u : 0u);
-          };
+        for (int k = 0; k < TK / 16; ++k) {
+          const int step = it * (TK / 16) + k, set = step % P.sets;
+          const bool add = step >= P.sets;
 #pragma unroll
-          for (int k = 0; k < TK / 16; ++k) {
-            mma(acc, 2, 0, k, it > 0 || k > 0);
-            mma(acc, 1, 1, k, true);
-            mma(acc, 0, 2, k, true);
-            mma(acc, 1, 0, k, true);
-            mma(acc, 0, 1, k, true);
-            mma(acc + (1 + main) * P.npc, 0, 0, k, it >= P.mains || k > 0);
+          for (int pw = 0; pw < 3; ++pw) {
+#pragma unroll
+            for (int i = 0; i < NW; ++i) {
+              const uint32_t acc = tmem + (i * P.sets + set) * P.orders * P.np;
+              const uint32_t wb = base + (i * 3 + pw) * PLANE;
+              const uint64_t a = MN ? tc::smem_desc(wb + k * 2048, PLANE / 2, 1024, tc::SWZ_128B)
+                                    : tc::smem_desc(wb + k * 32, 16, 512, tc::SWZ_64B);
+              const uint32_t xb = base + NW * 3 * PLANE + k * 32;
+              if (P.orders == 3) {
+                // X1 .. X(3 - pw), into the orders from pw on
+                tc::mma_bf16(acc + pw * P.np, a, tc::smem_desc(xb, 16, 512, tc::SWZ_64B),
+                             tc::idesc_bf16(TM, (3 - pw) * P.np, MN, false),
+                             add || pw > 0 ? 1u : 0u);
+              } else {
+                for (int px = 0; px < 3 - pw; ++px)
+                  tc::mma_bf16(acc + (pw + px > 0 ? P.np : 0), a,
+                               tc::smem_desc(xb + px * P.np * 64, 16, 512, tc::SWZ_64B),
+                               tc::idesc_bf16(TM, P.np, MN, false),
+                               add || pw > 0 || px > 1 ? 1u : 0u);
+              }
+            }
           }
         }
         tc::mma_commit(set_empty(s));
@@ -218,7 +230,11 @@ __global__ void __launch_bounds__(few32::NT, 1) k_ffn_few32(const __grid_constan
     }
   } else if (warp >= 4) {
     // -------------------------------------------------------------------- split
-    const int c = (threadIdx.x - 128) % (32 * NCONV);
+    // this thread's 16 bytes of each quarter of a tile: row r of 128 bytes, piece p,
+    // and where they go in a plane's first quarter
+    const int c = (threadIdx.x - 128) % (32 * NCONV), r = c >> 3, p = c & 7;
+    const int to0 = MN ? r * 128 + (((p >> 1) ^ (r & 7)) << 4) + (p & 1) * 8
+                       : r * 64 + (((p >> 1) ^ ((r >> 1) & 3)) << 4) + (p & 1) * 8;
     for (int it = (warp - 4) / NCONV; it < blocks; it += 2) {
       const int rs = it % P.raws, s = it & 1;
       bool ok = tc::mbar_pipe_wait<false>(raw_full(rs), (uint32_t)(it / P.raws) & 1u, abort_flag,
@@ -233,21 +249,13 @@ __global__ void __launch_bounds__(few32::NT, 1) k_ffn_few32(const __grid_constan
         const uint8_t* src = smem + (rs * NW + i) * RAW;
         uint8_t* dst = sets + s * set_bytes + i * 3 * PLANE;
 #pragma unroll
-        for (int e = 0; e < RAW / 16 / (32 * NCONV); ++e) {
-          // 16 bytes of the tile: row r of 128 bytes, piece p
-          const int at = c + e * 32 * NCONV, r = at >> 3, p = at & 7;
-          const float4 v = *reinterpret_cast<const float4*>(src + at * 16);
+        for (int e = 0; e < 4; ++e) {
           uint2 h, m, l;
-          split3x4(v, h, m, l);
-          int to;
-          if (MN) {
-            // tile [32 rows of W at a time][k][32]: r = 32 block + k
-            const int blk = r >> 5, k = r & 31;
-            to = (blk >> 1) * (PLANE / 2) + k * 128 +
-                 ((((blk & 1) * 4 + (p >> 1)) ^ (k & 7)) << 4) + (p & 1) * 8;
-          } else {
-            to = r * 64 + (((p >> 1) ^ ((r >> 1) & 3)) << 4) + (p & 1) * 8;
-          }
+          split3x4(*reinterpret_cast<const float4*>(src + c * 16 + e * (RAW / 4)), h, m, l);
+          // MN: quarter e is [k][32 of W's rows], every second one the upper half of
+          // the plane's 128-byte rows; else 32 rows
+          const int to = MN ? (to0 ^ ((e & 1) * 64)) + (e >> 1) * (PLANE / 2)
+                            : to0 + e * (PLANE / 4);
           *reinterpret_cast<uint2*>(dst + to) = h;
           *reinterpret_cast<uint2*>(dst + PLANE + to) = m;
           *reinterpret_cast<uint2*>(dst + 2 * PLANE + to) = l;
@@ -269,18 +277,18 @@ __global__ void __launch_bounds__(few32::NT, 1) k_ffn_few32(const __grid_constan
   if (warp < 4) {
     const int r = threadIdx.x;
     const uint32_t ta = tmem + ((uint32_t)(32 * warp) << 16);
-    const int used = blocks < P.mains ? blocks : P.mains;
+    // the lowest orders first, set by set
+    const int steps = blocks * (TK / 16), used = steps < P.sets ? steps : P.sets;
 #pragma unroll
     for (int i = 0; i < NW; ++i)
       for (int c = 0; c < P.np; c += 16) {
-        float v[16], m[16];
-        const uint32_t acc = ta + i * (1 + P.mains) * P.npc + c;
-        tc::tmem_get16(acc, v);
-        for (int q = 0; q < used; ++q) {
-          tc::tmem_get16(acc + (1 + q) * P.npc, m);
+        float v[16] = {}, m[16];
+        for (int o = P.orders - 1; o >= 0; --o)
+          for (int q = 0; q < used; ++q) {
+            tc::tmem_get16(ta + ((i * P.sets + q) * P.orders + o) * P.np + c, m);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] += m[e];
-        }
+            for (int e = 0; e < 16; ++e) v[e] += m[e];
+          }
 #pragma unroll
         for (int e = 0; e < 16; ++e) part[(i * P.np + c + e) * TM + r] = v[e];
       }
@@ -390,10 +398,10 @@ int sm_count() {
 
 int tokens16(int64_t t) { return (int)((t + 15) / 16 * 16); }
 
-// First-plane accumulators of a product with nw weights: what TMEM holds beside
-// the one of the other planes, up to four.
-int mains_of(int64_t t, int nw) {
-  const int npc = (tokens16(t) + 31) / 32 * 32, n = 512 / (nw * npc) - 1;
+// Accumulators per set, and sets per weight, of a product with nw weights.
+int orders_of(int64_t t, int nw) { return 3 * tokens16(t) * nw <= 512 && t <= 80 ? 3 : 2; }
+int sets_of(int64_t t, int nw) {
+  const int n = 512 / (nw * orders_of(t, nw) * tokens16(t));
   return n < 4 ? n : 4;
 }
 
@@ -406,10 +414,10 @@ cudaError_t launch(Few32P& P, const FewArgs& f, int64_t K, cudaStream_t s) {
   P.status = f.st;
   P.wait_ns = tc::wait_limit(f.wait_ns);
   P.kblocks = (int)((K + TK - 1) / TK);
-  P.npc = (uint32_t)((P.np + 31) / 32 * 32);
-  P.mains = mains_of(f.t, NW);
+  P.orders = orders_of(f.t, NW);
+  P.sets = sets_of(f.t, NW);
   P.tmem_cols = 32;
-  while (P.tmem_cols < NW * (1 + P.mains) * P.npc) P.tmem_cols *= 2;
+  while (P.tmem_cols < (uint32_t)(NW * P.sets * P.orders * P.np)) P.tmem_cols *= 2;
   const int sets = 2 * (NW * 3 * PLANE + 3 * P.np * TK * 2);
   P.raws = (ROOM - sets) / (NW * RAW);
   if (P.raws > MAXRAW) P.raws = MAXRAW;
@@ -420,7 +428,7 @@ cudaError_t launch(Few32P& P, const FewArgs& f, int64_t K, cudaStream_t s) {
   int parts = 0;
   int64_t best = 0;
   for (int p = 1; p <= 8 && p <= nk; p *= 2) {
-    if ((int64_t)(nk + p - 1) / p * TK > (int64_t)kMaxK * P.mains && p < 8 && 2 * p <= nk)
+    if ((int64_t)(nk + p - 1) / p * TK > (int64_t)kMaxK * P.sets && p < 8 && 2 * p <= nk)
       continue;
     const int64_t cost = ((tiles * p + slots - 1) / slots) * ((nk + p - 1) / p + 6);
     if (parts == 0 || cost < best) {
@@ -447,7 +455,7 @@ Few32P base(const FewArgs& f, int64_t rows, int nseg) {
 bool few32_fits(int64_t t, int64_t C, int64_t F) {
   if (t > kFewTokens32) return false;
   const int64_t one = (int64_t)8 * few32::kMaxK;
-  return C <= one * mains_of(t, 2) && 2 * F <= one * mains_of(t, 1);
+  return C <= one * sets_of(t, 2) && 2 * F <= one * sets_of(t, 1);
 }
 
 cudaError_t few32_gate(const FewArgs& f, void* a, float* g, float* u, cudaStream_t s) {

@@ -21,7 +21,7 @@
 // fp32 operands come as three bf16 planes each (their exact split, split3x4).  A
 // stage brings all planes of a 32-wide k block and six of the nine products of
 // planes are taken, those whose orders add up to at most two; what is left out is
-// below 2^-25 of a product.  The tensor cores' adder cuts instead of rounding,
+// 2^-24 of a product on average.  The tensor cores' adder cuts instead of rounding,
 // about half a unit of the last place per 16-wide step, which adds up over a long
 // sum (measured: 137 x 2^-24 at k = 5456).  So the first planes' products have
 // accumulators of their own, which they leave every kChunk k blocks to be added
