@@ -2,8 +2,8 @@
 //
 // As in k_ffn_few.cu the weights are the tall operand and are read once, 128 rows
 // per CTA, the k axis split over a cluster.  They arrive as they are, in fp32, by
-// TMA; two groups of eight warps split each 128 x 32 tile into its three bf16 planes (split3x4) in
-// shared memory, and the tensor cores take six of the nine products of planes with
+// TMA; sixteen warps split each 128 x 32 tile into its three bf16 planes (split3x4)
+// in shared memory, and the tensor cores take six of the nine products of planes with
 // the tokens' planes (what is left out is 2^-24 of a product on average).  Splitting
 // the weights beforehand, as the products of many tokens do, would move 16 bytes
 // per weight instead of 4.
@@ -19,9 +19,10 @@
 // to four sets of accumulators in turn, and a CTA's share of k is at most kMaxK per
 // set; the rest of the sum is rounded fp32 addition in the epilogue.
 //
-// Warps: 0 weights' TMA, 1 the MMAs, 2 the tokens' TMA, 4-11 and 12-19 the split of
-// the even and of the odd k blocks, each with a set of planes of its own; then all
-// of them the reduction over the cluster, as in k_ffn_few.cu.
+// Warps: 0 weights' TMA, 1 the MMAs, 2 the tokens' TMA, 4-19 the split; then all of
+// them the reduction over the cluster, as in k_ffn_few.cu.  Every warp takes part in
+// every k block: a waiter that skipped phases of a barrier could take an earlier
+// phase of the same parity for its own.
 #include "ffn_few.h"
 
 #include "ffn_common.cuh"
@@ -35,11 +36,11 @@ namespace few32 {
 constexpr int TM = 128, TK = 32;
 constexpr int RAW = TM * TK * 4;      // a weight tile in fp32
 constexpr int PLANE = TM * TK * 2;    // ... one of its planes
-constexpr int NT = 640, NCONV = 8;    // threads; splitting warps of a set of planes
+constexpr int NT = 640, NCONV = 16;   // threads; splitting warps
 constexpr int MAXRAW = 6;
 constexpr int ROOM = 222 * 1024, TAIL = 1024 + 512;
 constexpr int kMaxK = 2048;
-static_assert(RAW / 4 == 32 * NCONV * 16, "a thread takes 16 bytes of each quarter of a tile");
+static_assert(RAW / 2 == 32 * NCONV * 16, "a thread takes 16 bytes of each half of a tile");
 }  // namespace few32
 
 enum Epi32 { F32_STORE, F32_GATE, F32_DGATE };
@@ -230,12 +231,12 @@ __global__ void __launch_bounds__(few32::NT, 1) k_ffn_few32(const __grid_constan
     }
   } else if (warp >= 4) {
     // -------------------------------------------------------------------- split
-    // this thread's 16 bytes of each quarter of a tile: row r of 128 bytes, piece p,
-    // and where they go in a plane's first quarter
-    const int c = (threadIdx.x - 128) % (32 * NCONV), r = c >> 3, p = c & 7;
-    const int to0 = MN ? r * 128 + (((p >> 1) ^ (r & 7)) << 4) + (p & 1) * 8
+    // this thread's 16 bytes of each half of a tile (row r of 128 bytes, piece p),
+    // and where they go in a half of a plane
+    const int c = threadIdx.x - 128, r = c >> 3, p = c & 7, k = r & 31;
+    const int to0 = MN ? k * 128 + ((((r >> 5) * 4 + (p >> 1)) ^ (k & 7)) << 4) + (p & 1) * 8
                        : r * 64 + (((p >> 1) ^ ((r >> 1) & 3)) << 4) + (p & 1) * 8;
-    for (int it = (warp - 4) / NCONV; it < blocks; it += 2) {
+    for (int it = 0; it < blocks; ++it) {
       const int rs = it % P.raws, s = it & 1;
       bool ok = tc::mbar_pipe_wait<false>(raw_full(rs), (uint32_t)(it / P.raws) & 1u, abort_flag,
                                           P.wait_ns);
@@ -249,13 +250,12 @@ __global__ void __launch_bounds__(few32::NT, 1) k_ffn_few32(const __grid_constan
         const uint8_t* src = smem + (rs * NW + i) * RAW;
         uint8_t* dst = sets + s * set_bytes + i * 3 * PLANE;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 2; ++e) {
           uint2 h, m, l;
-          split3x4(*reinterpret_cast<const float4*>(src + c * 16 + e * (RAW / 4)), h, m, l);
-          // MN: quarter e is [k][32 of W's rows], every second one the upper half of
-          // the plane's 128-byte rows; else 32 rows
-          const int to = MN ? (to0 ^ ((e & 1) * 64)) + (e >> 1) * (PLANE / 2)
-                            : to0 + e * (PLANE / 4);
+          split3x4(*reinterpret_cast<const float4*>(src + c * 16 + e * (RAW / 2)), h, m, l);
+          // K-major: 64 rows further; MN: the tile is [32 rows of W at a time][k][32]
+          // and the plane [64 rows at a time][k][64]
+          const int to = to0 + e * (PLANE / 2);
           *reinterpret_cast<uint2*>(dst + to) = h;
           *reinterpret_cast<uint2*>(dst + PLANE + to) = m;
           *reinterpret_cast<uint2*>(dst + 2 * PLANE + to) = l;
