@@ -1,5 +1,5 @@
 // ffn_few.h -- the feed-forward products of few tokens: bf16 in k_ffn_few.cu, fp32
-// in k_ffn_few32.cu.
+// in k_ffn_one32.cu (up to 8) and k_ffn_few32.cu.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -36,5 +36,16 @@ cudaError_t few32_gate(const FewArgs& f, void* a, float* g, float* u, cudaStream
 cudaError_t few32_down(const FewArgs& f, const void* a, float* y, cudaStream_t s);
 cudaError_t few32_dgate(const FewArgs& f, const float* g, const float* u, void* d, cudaStream_t s);
 cudaError_t few32_grad_x(const FewArgs& f, const void* d, float* gx, cudaStream_t s);
+
+// k_ffn_one32.cu: the same on the CUDA cores, up to this many tokens, from the
+// caller's fp32 arrays; the planes of a and of dg, du are for the weight gradients
+// (a or its planes may be null).
+constexpr int64_t kOneTokens = 8;
+cudaError_t one32_gate(const FewArgs& f, float* a, void* planes, float* g, float* u,
+                       cudaStream_t s);
+cudaError_t one32_down(const FewArgs& f, const float* a, float* y, cudaStream_t s);
+cudaError_t one32_dgate(const FewArgs& f, const float* g, const float* u, float* d, void* planes,
+                        cudaStream_t s);
+cudaError_t one32_grad_x(const FewArgs& f, const float* d, float* gx, cudaStream_t s);
 
 }  // namespace mhc

@@ -656,7 +656,11 @@ struct Ffn {
   const void *x, *wg, *wu, *wd, *gy;
   int* st;
   int64_t wait_ns;
-  bool is_few() const { return np == 3 ? few32_fits(t, C, F) : t <= kFewTokens; }
+  // fp32 inputs before their split (k_ffn_one32.cu reads them)
+  const void *x32, *gy32;
+  bool is_one() const { return np == 3 && t <= kOneTokens; }
+  FewArgs one() const { return {t, C, F, act, x32, wg, wu, wd, gy32, st, wait_ns}; }
+  bool is_few() const { return np == 3 ? is_one() || few32_fits(t, C, F) : t <= kFewTokens; }
   FewArgs few() const { return {t, C, F, act, x, wg, wu, wd, gy, st, wait_ns}; }
 };
 
@@ -689,6 +693,10 @@ template <bool F32> cudaError_t gate_product(const Ffn& f, void* a, float* g, fl
 template <bool F32> cudaError_t fwd(const Ffn& f, void* y, void* a, cudaStream_t s) {
   if (f.is_few()) {
     if constexpr (F32) {
+      if (f.is_one()) {
+        TRY(one32_gate(f.one(), (float*)a, nullptr, nullptr, nullptr, s));
+        return one32_down(f.one(), (const float*)a, (float*)y, s);
+      }
       TRY(few32_gate(f.few(), a, nullptr, nullptr, s));
       return few32_down(f.few(), a, (float*)y, s);
     } else {
@@ -705,15 +713,18 @@ template <bool F32> cudaError_t fwd(const Ffn& f, void* y, void* a, cudaStream_t
 
 // a [np][t][F], d [2 np][t][F] (dg, du), g and u [t][F].
 template <bool F32>
-cudaError_t bwd(const Ffn& f, void* gx, void* gwg, void* gwu, void* gwd, void* a, void* d, float* g,
-                float* u, cudaStream_t s) {
+cudaError_t bwd(const Ffn& f, void* gx, void* gwg, void* gwu, void* gwd, void* a, void* d,
+                float* d32, float* g, float* u, cudaStream_t s) {
   const int np = f.np;
   const Mat X{f.x, f.t, f.C, np, false}, GY{f.gy, f.t, f.C, np, false};
   const Mat A{a, f.t, f.F, np, false}, D{d, f.t, f.F, 2 * np, false};
   const Mat WG{f.wg, f.F, f.C, np, false}, WU{f.wu, f.F, f.C, np, false};
   const Mat WD{f.wd, f.C, f.F, np, false};
   const bool few = f.is_few();
-  if (few && F32) {
+  if (f.is_one()) {
+    TRY(one32_gate(f.one(), nullptr, a, g, u, s));
+    TRY(one32_dgate(f.one(), g, u, d32, d, s));
+  } else if (few && F32) {
     TRY(few32_gate(f.few(), a, g, u, s));
     TRY(few32_dgate(f.few(), g, u, d, s));
   } else if (few) {
@@ -729,7 +740,9 @@ cudaError_t bwd(const Ffn& f, void* gx, void* gwg, void* gwu, void* gwd, void* a
   }
   // the rest needs only what is finished when the next kernel starts: the three
   // run beside one another, each filling the SMs that the one before leaves idle
-  if (few && F32) {
+  if (f.is_one()) {
+    TRY(one32_grad_x(f.one(), d32, (float*)gx, s));
+  } else if (few && F32) {
     TRY(few32_grad_x(f.few(), d, (float*)gx, s));
   } else if (few) {
     TRY(few_grad_x(f.few(), d, gx, s));
@@ -759,7 +772,7 @@ size_t up(size_t v) { return (v + 255) / 256 * 256; }
 // also of dg and du, and g and u in fp32.  fp32: the split copies of the inputs
 // (with few tokens the weights are split on their way into the products).
 struct Layout {
-  size_t a, d, g, u, x, wg, wu, wd, gy, total;
+  size_t a, d, d32, g, u, x, wg, wu, wd, gy, total;
 };
 Layout layout(bool f32, bool backward, int64_t t, int64_t C, int64_t F) {
   Layout w{};
@@ -775,11 +788,12 @@ Layout layout(bool f32, bool backward, int64_t t, int64_t C, int64_t F) {
     w.d = take(hid * 2 * 2 * np);
     w.g = take(hid * 4);
     w.u = take(hid * 4);
+    if (f32 && t <= kOneTokens) w.d32 = take(hid * 8);
   }
   if (f32) {
     w.x = take(io * 6);
     if (backward) w.gy = take(io * 6);
-    if (!few32_fits(t, C, F)) {
+    if (t > kOneTokens && !few32_fits(t, C, F)) {
       w.wg = take(wt * 6);
       w.wu = take(wt * 6);
       w.wd = take(wt * 6);
@@ -793,6 +807,9 @@ Layout layout(bool f32, bool backward, int64_t t, int64_t C, int64_t F) {
 cudaError_t operands(Ffn& f, bool f32, const Layout& w, char* ws, cudaStream_t s) {
   f.np = f32 ? 3 : 1;
   if (!f32) return cudaSuccess;
+  f.x32 = f.x;
+  f.gy32 = f.gy;
+  if (f.is_one() && !f.gy) return cudaSuccess;  // the forward takes them as they are
   const int64_t io = f.t * f.C, wt = f.F * f.C;
   SplitArgs a{};
   auto add = [&](const void*& p, size_t off, int64_t n) {
@@ -827,7 +844,7 @@ cudaError_t ffn_fwd_dispatch(int dtype, int act, int64_t t, int64_t C, int64_t F
                              int* st, int64_t wait_ns, cudaStream_t s) {
   const bool f32 = dtype != MHC_DTYPE_BF16;
   const Layout w = layout(f32, false, t, C, F);
-  Ffn f{t, C, F, act, 1, x, wg, wu, wd, nullptr, st, wait_ns};
+  Ffn f{t, C, F, act, 1, x, wg, wu, wd, nullptr, st, wait_ns, nullptr, nullptr};
   TRY(operands(f, f32, w, (char*)ws, s));
   char* b = (char*)ws;
   return f32 ? fwd<true>(f, y, b + w.a, s) : fwd<false>(f, y, b + w.a, s);
@@ -839,12 +856,12 @@ cudaError_t ffn_bwd_dispatch(int dtype, int act, int64_t t, int64_t C, int64_t F
                              int64_t wait_ns, cudaStream_t s) {
   const bool f32 = dtype != MHC_DTYPE_BF16;
   const Layout w = layout(f32, true, t, C, F);
-  Ffn f{t, C, F, act, 1, x, wg, wu, wd, gy, st, wait_ns};
+  Ffn f{t, C, F, act, 1, x, wg, wu, wd, gy, st, wait_ns, nullptr, nullptr};
   char* b = (char*)ws;
   TRY(operands(f, f32, w, b, s));
-  float *g = (float*)(b + w.g), *u = (float*)(b + w.u);
-  return f32 ? bwd<true>(f, gx, gwg, gwu, gwd, b + w.a, b + w.d, g, u, s)
-             : bwd<false>(f, gx, gwg, gwu, gwd, b + w.a, b + w.d, g, u, s);
+  float *g = (float*)(b + w.g), *u = (float*)(b + w.u), *d32 = (float*)(b + w.d32);
+  return f32 ? bwd<true>(f, gx, gwg, gwu, gwd, b + w.a, b + w.d, d32, g, u, s)
+             : bwd<false>(f, gx, gwg, gwu, gwd, b + w.a, b + w.d, nullptr, g, u, s);
 }
 
 #undef TRY

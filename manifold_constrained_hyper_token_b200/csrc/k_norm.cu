@@ -16,6 +16,8 @@
 // elements (T = 16384, C = 7168 bf16: 187 us forward, 455 us backward).  So a
 // thread takes up to 64 channels (forward) or 32 (backward) and works on pairs of
 // floats (the paired fp32 instructions).
+#include <algorithm>
+
 #include "mhc_common.cuh"
 #include "mhc_dispatch.h"
 #include "tc_pair.cuh"
@@ -108,6 +110,21 @@ template <int N> __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Sums over the warp of a (row 0) and b (row 1): lanes 0..15 get row 0's, lanes
+// 16..31 row 1's.
+__device__ __forceinline__ float pair_sum(float a, float b, int lane) {
+  const bool hi = lane >= 16;
+  float v = (hi ? b : a) + __shfl_xor_sync(0xffffffffu, hi ? a : b, 16);
+#pragma unroll
+  for (int o = 8; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float half_sum(float v) {
+#pragma unroll
+  for (int o = 8; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
 // ------------------------------------------------------------------ forward
 // WARP: one row per warp (blockDim.x / 32 rows per CTA); otherwise one row per
 // CTA.  A thread holds VPT 16-byte vectors of its row.
@@ -179,6 +196,125 @@ __global__ void __launch_bounds__(MAXT)
       for (int e = 0; e < P; ++e)
         o[e] = f2fma(f2fma(v[i][e], ss, nms), wv[e], bv[e]);
       __stcs(yr + k, PV::pack(o));
+    }
+  }
+}
+
+// Many rows: persistent CTAs that take two rows at a time, as the backward does (see
+// there), through a ring of two row pairs in shared memory.  Two rows share the
+// loads of weight and bias and half the shuffles, and a CTA's fixed work is paid
+// once: T = 16384, C = 7168 bf16 has XX instructions per row instead of 3050.
+template <typename T, int VPT, bool WARP, int MAXT, int PERSM>
+__global__ void __launch_bounds__(MAXT, PERSM)
+    k_norm_fwd_pairs(int64_t rows, int64_t C, float eps, const T* __restrict__ x,
+                     const float* __restrict__ w, const float* __restrict__ b, T* __restrict__ y,
+                     int* status) {
+  constexpr int N = Vec<T>::N, P = Pairs<T>::P;
+  using PV = Pairs<T>;
+  __shared__ float2 rec[WARP ? 1 : 2][2][16];
+  extern __shared__ uint4 ring[];  // [group][2][row][nvec]
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int tpr = WARP ? 32 : blockDim.x;
+  const int t = WARP ? lane : threadIdx.x;
+  const int per = WARP ? blockDim.x / 32 : 1, g = WARP ? warp : 0;
+  const int nvec = (int)(C / N);
+  uint4* mine = ring + (int64_t)g * 4 * nvec;
+  const int64_t row0 = 2 * ((int64_t)blockIdx.x * per + g), step = 2 * (int64_t)gridDim.x * per;
+  const float inv_c = 1.0f / (float)C;
+  const float inv_n = WARP ? inv_c : inv_or_0(share_channels(warp, tpr, N, nvec));
+  const float nq =
+      WARP || (lane & 15) >= tpr / 32 ? 0.f : share_channels(lane & 15, tpr, N, nvec);
+  tc::grid_wait();
+  auto fetch = [&](int64_t row, int slot) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      if (row + r < rows) {
+        uint4* d = mine + (slot * 2 + r) * nvec;
+        const uint4* xr = reinterpret_cast<const uint4*>(x + (row + r) * C);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+          const int k = t + i * tpr;
+          if (k < nvec) cp16(d + k, xr + k);
+        }
+      }
+    }
+    cp_commit();
+  };
+  fetch(row0, 0);
+  int it = 0;
+  for (int64_t row = row0; row < rows; row += step, ++it) {
+    const int slot = it & 1;
+    fetch(row + step, slot ^ 1);
+    cp_wait<1>();
+    const bool two = row + 1 < rows;
+    const uint4* xs[2] = {mine + slot * 2 * nvec, mine + (slot * 2 + (two ? 1 : 0)) * nvec};
+    uint64_t v[2][VPT][P], sum[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int k = t + i * tpr;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint4 q = k < nvec ? xs[r][k] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+          v[r][i][e] = PV::get(q, e);
+          sum[r] = f2add(sum[r], v[r][i][e]);
+        }
+      }
+    }
+    // from here to the join a lane's scalars are its half-warp's row's
+    float m = pair_sum(f2sum(sum[0]), f2sum(sum[1]), lane) * inv_n;
+    const uint64_t nm[2] = {f2dup(-__shfl_sync(0xffffffffu, m, 0)),
+                            f2dup(-__shfl_sync(0xffffffffu, m, 16))};
+    uint64_t m2[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      if (t + i * tpr < nvec) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int e = 0; e < P; ++e) {
+            const uint64_t d = f2add(v[r][i][e], nm[r]);
+            m2[r] = f2fma(d, d, m2[r]);
+          }
+      }
+    }
+    float v2 = pair_sum(f2sum(m2[0]), f2sum(m2[1]), lane);
+    if (!WARP) {
+      if ((lane & 15) == 0) rec[it & 1][lane >> 4][warp] = make_float2(m, v2);
+      __syncthreads();
+      const float2 q = nq > 0.f ? rec[it & 1][lane >> 4][lane & 15] : make_float2(0.f, 0.f);
+      m = half_sum(nq * q.x) * inv_c;
+      const float d = q.x - m;
+      v2 = half_sum(q.y + nq * d * d);
+    }
+    const float s = rsqrtf(v2 * inv_c + eps);
+    if (t == 0 || (t == 16 && two)) report(m, s, status);
+    uint64_t ss[2], nms[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      ss[r] = f2dup(__shfl_sync(0xffffffffu, s, 16 * r));
+      nms[r] = f2dup(__shfl_sync(0xffffffffu, -m * s, 16 * r));
+    }
+    uint4* yr = reinterpret_cast<uint4*>(y + row * C);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int k = t + i * tpr;
+      if (k < nvec) {
+        uint64_t wv[P], bv[P] = {};
+        load_param<P>(w + k * N, wv);
+        if (b) load_param<P>(b + k * N, bv);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          if (r == 0 || two) {
+            uint64_t o[P];
+#pragma unroll
+            for (int e = 0; e < P; ++e)
+              o[e] = f2fma(f2fma(v[r][i][e], ss[r], nms[r]), wv[e], bv[e]);
+            __stcs(yr + r * nvec + k, PV::pack(o));
+          }
+        }
+      }
     }
   }
 }
@@ -257,21 +393,6 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_fwd_long(
 // through a ring of two row pairs in shared memory (cp.async: a thread copies
 // what it later reads itself, so no barrier is needed).  WARP: a pair of rows per
 // warp, the warps' sums joined in warp order through the ring's memory.
-
-// Sums over the warp of a (row 0) and b (row 1): lanes 0..15 get row 0's, lanes
-// 16..31 row 1's.
-__device__ __forceinline__ float pair_sum(float a, float b, int lane) {
-  const bool hi = lane >= 16;
-  float v = (hi ? b : a) + __shfl_xor_sync(0xffffffffu, hi ? a : b, 16);
-#pragma unroll
-  for (int o = 8; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-__device__ __forceinline__ float half_sum(float v) {
-#pragma unroll
-  for (int o = 8; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
 
 template <typename T, int VPT, bool WARP, int MAXT, int PERSM>
 __global__ void __launch_bounds__(MAXT, PERSM)
@@ -578,13 +699,46 @@ int sm_count() {
 int round32(int64_t v) { return (int)((v + 31) / 32 * 32); }
 
 // Partial rows of grad_weight / grad_bias: the workspace is sized for this many.
-constexpr int kMaxParts = 480;
+constexpr int kMaxParts = 592;
 constexpr int64_t kLongRow = 56 * 1024;  // bytes of x and gy: longer rows are walked in memory
+
+// CTAs of `threads` threads and `smem` bytes that an SM holds, at 128 registers a
+// thread (2 KB of shared memory beside: 1 KB of records, 1 KB of the system's), and
+// at most `most`.
+int resident(int threads, size_t smem, int most) {
+  const int by_regs = 512 / threads, by_smem = (int)(233472 / (smem + 2048));
+  return std::max(1, std::min(most, std::min(by_regs, by_smem)));
+}
+
+template <typename T, int VPT, bool WARP, int MAXT, int PERSM>
+cudaError_t fwd_pairs(int64_t rows, int64_t C, float eps, const T* x, const float* w,
+                      const float* b, T* y, int threads, int* st, cudaStream_t s) {
+  const int per = WARP ? threads / 32 : 1;
+  const size_t sm = (size_t)per * 4 * C * sizeof(T);
+  const int64_t groups = (rows + 2 * per - 1) / (2 * per);
+  const int64_t g = (int64_t)sm_count() * resident(threads, sm, 8);
+  auto kern = k_norm_fwd_pairs<T, VPT, WARP, MAXT, PERSM>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+  if (e != cudaSuccess) return e;
+  return launch_after(kern, (unsigned)(groups < g ? groups : g), (unsigned)threads, sm, 1, s, rows,
+                      C, eps, x, w, b, y, st);
+}
 
 template <typename T>
 cudaError_t fwd(int64_t rows, int64_t C, float eps, const T* x, const float* w, const float* b,
                 T* y, int* st, cudaStream_t s) {
   const int64_t nvec = C / Vec<T>::N;
+  constexpr int V = 32 / Vec<T>::N;  // vectors of a thread
+  const int threads = round32((nvec + V - 1) / V);
+  // fp32 rows have half the arithmetic per byte and run faster one to a CTA (T =
+  // 8192, C = 4096: 49 us against 61)
+  if (sizeof(T) == 2 && rows >= 16 * sm_count()) {
+    if (C > 512 && C <= 1024)
+      return fwd_pairs<T, V, true, 128, 4>(rows, C, eps, x, w, b, y, 128, st, s);
+    if (C > 1024 && C <= 8192)
+      return fwd_pairs<T, V, false, 256, 2>(rows, C, eps, x, w, b, y, threads, st, s);
+  }
   if (nvec > 8 * 512) {
     k_norm_fwd_long<T><<<(unsigned)rows, kMaxThreads, 0, s>>>(C, eps, x, w, b, y, st);
     return cudaGetLastError();
@@ -609,8 +763,7 @@ cudaError_t bwd_rows(int64_t rows, int64_t C, float eps, const T* x, const float
   const size_t ring = (size_t)per * 8 * C * sizeof(T);
   const size_t sum = WARP ? (size_t)2 * C * 4 : 0, sm = ring > sum ? ring : sum;
   const int64_t groups = (rows + 2 * per - 1) / (2 * per);
-  int64_t g = (int64_t)sm_count() * PERSM;
-  if (g > kMaxParts) g = kMaxParts;
+  const int64_t g = std::min<int64_t>(kMaxParts, (int64_t)sm_count() * resident(threads, sm, 4));
   *nparts = (int)(groups < g ? groups : g);
   auto kern = k_norm_bwd<T, VPT, WARP, MAXT, PERSM>;
   cudaError_t e =
@@ -620,18 +773,19 @@ cudaError_t bwd_rows(int64_t rows, int64_t C, float eps, const T* x, const float
                       gx, part, st);
 }
 
-// 32 channels per thread: rows of up to 1024 channels on one warp, longer ones on
-// a CTA of which two fit an SM (up to 7168 channels in bf16, 3584 in fp32) or one
-// (twice that); what is longer does not fit the ring.
+// Rows of up to 1024 channels on one warp; longer ones on a CTA, four vectors per
+// thread (32 channels in bf16, 16 in fp32, whose rows leave shared memory for fewer
+// CTAs), up to 14336 channels in bf16 and 7168 in fp32; what is longer does not fit
+// the ring.
 template <typename T>
 cudaError_t bwd(int64_t rows, int64_t C, float eps, const T* x, const float* w, const T* gy, T* gx,
                 float* gw, float* gb, void* ws, int* st, cudaStream_t s) {
-  constexpr int V = 32 / Vec<T>::N;  // vectors of a thread
+  constexpr int V = 32 / Vec<T>::N;  // vectors of a lane at 1024 channels
   const int64_t nvec = C / Vec<T>::N, row = 2 * C * (int64_t)sizeof(T);  // x and gy
   float* part = (float*)ws;
   int nparts = 0;
   cudaError_t e;
-  const int threads = round32((nvec + V - 1) / V);
+  const int threads = round32((nvec + 3) / 4);
   if (row > kLongRow) {
     float2* stat = (float2*)(part + (int64_t)kMaxParts * 2 * C);
     k_norm_bwd_long<T><<<(unsigned)rows, kMaxThreads, 0, s>>>(C, eps, x, w, gy, gx, stat, st);
@@ -647,10 +801,10 @@ cudaError_t bwd(int64_t rows, int64_t C, float eps, const T* x, const float* w, 
     e = bwd_rows<T, V / 2, true, 128, 3>(rows, C, eps, x, w, gy, gx, part, 128, &nparts, st, s);
   } else if (C <= 1024) {
     e = bwd_rows<T, V, true, 96, 2>(rows, C, eps, x, w, gy, gx, part, 96, &nparts, st, s);
-  } else if (row <= 28 * 1024 && threads <= 256) {
-    e = bwd_rows<T, V, false, 256, 2>(rows, C, eps, x, w, gy, gx, part, threads, &nparts, st, s);
+  } else if (threads <= 256) {
+    e = bwd_rows<T, 4, false, 256, 2>(rows, C, eps, x, w, gy, gx, part, threads, &nparts, st, s);
   } else {
-    e = bwd_rows<T, V, false, 512, 1>(rows, C, eps, x, w, gy, gx, part, threads, &nparts, st, s);
+    e = bwd_rows<T, 4, false, 512, 1>(rows, C, eps, x, w, gy, gx, part, threads, &nparts, st, s);
   }
   if (e != cudaSuccess) return e;
   const int64_t cols = 2 * C / 4;
