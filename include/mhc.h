@@ -466,9 +466,13 @@ typedef struct mhc_ffn_params {
  *        weights per output unit)
  *   out: y [T][C]
  * Sums run in float32.  With bf16 the product a is rounded to bf16 once
- * between the two matrix products.  workspace: at least
- * mhc_ffn_workspace_size(p) bytes, 256-byte aligned; its contents on entry do
- * not matter.  Repeated calls give identical bits.
+ * between the two matrix products.  With fp32 and more than 8 tokens the
+ * products run on the tensor cores, each operand as the exact sum of three
+ * bf16 numbers: relative to the sum of absolute products about 2^-24 from the
+ * terms left out and 2^-19 from the adder over long sums; magnitudes below
+ * 2^-110 lose bits.  A token that is not finite spoils its own row of y only.
+ * workspace: at least mhc_ffn_workspace_size(p) bytes, 256-byte aligned; its
+ * contents on entry do not matter.  Repeated calls give identical bits.
  */
 MHC_API size_t mhc_ffn_workspace_size(const mhc_ffn_params *p);
 MHC_API mhc_status mhc_ffn(const mhc_ffn_params *p, const void *x, const void *w_gate,
@@ -484,10 +488,11 @@ MHC_API mhc_status mhc_ffn(const mhc_ffn_params *p, const void *x, const void *w
  *   in : x [T][C], w_gate, w_up [F][C], w_down [C][F], grad_y [T][C]
  *   out: grad_x [T][C], grad_w_gate, grad_w_up [F][C], grad_w_down [C][F]
  *        (OVERWRITTEN), all of the call's dtype
- * Sums run in float32 and are rounded once at the end.  With bf16 the
- * intermediates g, u, a, dg and du are rounded to bf16.  workspace: at least
- * mhc_ffn_backward_workspace_size(p) bytes, 256-byte aligned; its contents on
- * entry do not matter.  Repeated calls give identical bits.
+ * Sums run in float32 and are rounded once at the end (fp32: as in mhc_ffn).
+ * With bf16 the intermediates a, dg and du are rounded to bf16; g and u stay in
+ * float32.  workspace: at least mhc_ffn_backward_workspace_size(p) bytes,
+ * 256-byte aligned; its contents on entry do not matter.  Repeated calls give
+ * identical bits.
  */
 MHC_API size_t mhc_ffn_backward_workspace_size(const mhc_ffn_params *p);
 MHC_API mhc_status mhc_ffn_backward(const mhc_ffn_params *p, const void *x, const void *w_gate,

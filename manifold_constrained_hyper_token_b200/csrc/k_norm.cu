@@ -12,10 +12,11 @@
 // difference of large sums, and one block barrier per row.
 //
 // What is left to care about is the number of instructions: with 16 channels per
-// thread and scalar arithmetic the shuffles and joins of a row cost more than its
+// thread and a row at a time the shuffles and joins of a row cost more than its
 // elements (T = 16384, C = 7168 bf16: 187 us forward, 455 us backward).  So a
-// thread takes up to 64 channels (forward) or 32 (backward) and works on pairs of
-// floats (the paired fp32 instructions).
+// thread takes 32 channels or 64 and, where there are many rows, two rows at a
+// time, in paired fp32 instructions: 96 us (4.9 TB/s) and 165 us (4.3 TB/s).  The
+// backward is held back by the weight: the ring leaves the L1 less than its 28 KB.
 #include <algorithm>
 
 #include "mhc_common.cuh"
@@ -203,7 +204,7 @@ __global__ void __launch_bounds__(MAXT)
 // Many rows: persistent CTAs that take two rows at a time, as the backward does (see
 // there), through a ring of two row pairs in shared memory.  Two rows share the
 // loads of weight and bias and half the shuffles, and a CTA's fixed work is paid
-// once: T = 16384, C = 7168 bf16 has XX instructions per row instead of 3050.
+// once: T = 16384, C = 7168 bf16 takes 98 us against 106 with a row per CTA.
 template <typename T, int VPT, bool WARP, int MAXT, int PERSM>
 __global__ void __launch_bounds__(MAXT, PERSM)
     k_norm_fwd_pairs(int64_t rows, int64_t C, float eps, const T* __restrict__ x,
@@ -698,9 +699,13 @@ int sm_count() {
 
 int round32(int64_t v) { return (int)((v + 31) / 32 * 32); }
 
-// Partial rows of grad_weight / grad_bias: the workspace is sized for this many.
-constexpr int kMaxParts = 592;
-constexpr int64_t kLongRow = 56 * 1024;  // bytes of x and gy: longer rows are walked in memory
+// Partial rows of grad_weight and grad_bias: at most one per pair of rows and
+// kMaxParts; kLongParts where a row's x and gy, more than kLongRow bytes, are walked
+// in memory.
+constexpr int64_t kMaxParts = 592, kLongParts = 64, kLongRow = 56 * 1024;
+int64_t most_parts(int64_t rows, int64_t row_bytes) {
+  return row_bytes > kLongRow ? std::min(rows, kLongParts) : std::min((rows + 1) / 2, kMaxParts);
+}
 
 // CTAs of `threads` threads and `smem` bytes that an SM holds, at 128 registers a
 // thread (2 KB of shared memory beside: 1 KB of records, 1 KB of the system's), and
@@ -764,7 +769,7 @@ cudaError_t bwd_rows(int64_t rows, int64_t C, float eps, const T* x, const float
   const size_t sum = WARP ? (size_t)2 * C * 4 : 0, sm = ring > sum ? ring : sum;
   const int64_t groups = (rows + 2 * per - 1) / (2 * per);
   const int64_t g = std::min<int64_t>(kMaxParts, (int64_t)sm_count() * resident(threads, sm, 4));
-  *nparts = (int)(groups < g ? groups : g);
+  *nparts = (int)(groups < g ? groups : g);  // at most most_parts()
   auto kern = k_norm_bwd<T, VPT, WARP, MAXT, PERSM>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
@@ -787,11 +792,11 @@ cudaError_t bwd(int64_t rows, int64_t C, float eps, const T* x, const float* w, 
   cudaError_t e;
   const int threads = round32((nvec + 3) / 4);
   if (row > kLongRow) {
-    float2* stat = (float2*)(part + (int64_t)kMaxParts * 2 * C);
+    nparts = (int)most_parts(rows, row);
+    float2* stat = (float2*)(part + (int64_t)nparts * 2 * C);
     k_norm_bwd_long<T><<<(unsigned)rows, kMaxThreads, 0, s>>>(C, eps, x, w, gy, gx, stat, st);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    nparts = (int)(rows < 64 ? rows : 64);
     const dim3 grid((unsigned)((nvec + 255) / 256), (unsigned)nparts);
     k_norm_bwd_cols<T><<<grid, 256, 0, s>>>(rows, C, x, gy, stat, part);
     e = cudaGetLastError();
@@ -816,7 +821,8 @@ cudaError_t bwd(int64_t rows, int64_t C, float eps, const T* x, const float* w, 
 
 size_t norm_bwd_workspace_bytes(int64_t rows, int64_t C, int dtype) {
   const int64_t row = 2 * C * (dtype == MHC_DTYPE_BF16 ? 2 : 4);
-  return (size_t)kMaxParts * 2 * C * 4 + (row > kLongRow ? (size_t)rows * sizeof(float2) : 0);
+  return (size_t)most_parts(rows, row) * 2 * C * 4 +
+         (row > kLongRow ? (size_t)rows * sizeof(float2) : 0);
 }
 
 cudaError_t norm_fwd_dispatch(int dtype, int64_t rows, int64_t C, float eps, const void* x,

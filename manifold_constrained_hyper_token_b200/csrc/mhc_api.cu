@@ -11,7 +11,7 @@
 namespace {
 
 constexpr int kVersionMajor = 0;
-constexpr int kVersionMinor = 2;
+constexpr int kVersionMinor = 3;
 
 bool aligned16(const void* p) { return p != nullptr && ((uintptr_t)p & 15u) == 0; }
 

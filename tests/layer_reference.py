@@ -6,8 +6,12 @@ Every bound is propagated through the operator step by step in absolute values:
 * u = 2^-24: one fp32 rounding, relative.  A tensor-core sum may cut instead of
   round; that is one step, 2u, but it adds 16 products at a time, so (k + 16) u
   times the sum of absolute products covers a sum of k terms either way (fp32
-  operands are split in three bf16 parts and take six passes: 6 k / 16 additions
-  of 2u each, below k u; what the split leaves out is below 2^-23).
+  operands are split in three bf16 parts by cutting and take six passes: 6 k / 16
+  additions of 2u each, 0.75 k u; the parts are below 2^-7 and 2^-15 of the whole, so the
+  three products left out are below 2 2^-22 + 2^-30 = 8u of a product: inside the 16 u).
+* GRID = 2^-133: bf16's smallest step.  The last of an fp32 operand's three bf16 parts is
+  cut to it, so an operand is off by up to GRID absolutely: |x| = 3.3e38 against a weight
+  of 1e-39 makes that 3.3e38 2^-133 = 0.03 of a product of 0.3, and nothing otherwise.
 * r: the rounding of a stored value, half a step of its type: 2^-8 relative for
   bf16, u for fp32.
 * the norm's row sums run over at most 32 values per thread in order, five
@@ -20,6 +24,7 @@ import math
 import torch
 
 U = 2.0 ** -24
+GRID = 2.0 ** -133
 HALF_STEP = {torch.bfloat16: 2.0 ** -8, torch.float32: U}
 
 
@@ -105,14 +110,23 @@ def ffn_grad(x, wg, wu, wd, gy, act):
     return dg @ wg + du @ wu, dg.T @ x, du.T @ x, gy.T @ (h * u)
 
 
+def _sum_err(a, b, dtype, terms=None):
+    """Bound on the error of a kernel's a @ b, given a and b exactly; terms: the sum's length
+    where it goes on beyond a and b."""
+    a, b = a.abs(), b.abs()
+    e = ((terms or a.shape[1]) + 16) * U * (a @ b)
+    if dtype == torch.float32:
+        e = e + GRID * (a.sum(1, keepdim=True) + b.sum(0, keepdim=True))
+    return e
+
+
 def _inner(x, wg, wu, act, dtype, store):
     """g, u, h, dh and bounds on them; store: g and u are kept in the call's type."""
-    k = (x.shape[1] + 16) * U
     fn = 16 * U if dtype == torch.float32 else 2.0 ** -18
     r = HALF_STEP[dtype] if store else 0.0
     g, u = x @ wg.T, x @ wu.T
-    dg = k * (x.abs() @ wg.abs().T)
-    du = k * (x.abs() @ wu.abs().T)
+    dg = _sum_err(x, wg.T, dtype)
+    du = _sum_err(x, wu.T, dtype)
     dg, du = dg + r * (g.abs() + dg), du + r * (u.abs() + du)
     h, dh = gate(g, act)
     eh = 1.2 * dg + fn * g.abs()
@@ -127,14 +141,13 @@ def ffn_bound(x, wg, wu, wd, act, dtype):
     a = h * u
     ea = eh * (u.abs() + eu) + h.abs() * eu
     ea = ea + r * (a.abs() + ea) + 2 * U * a.abs()
-    d = ea @ wd.abs().T + (wd.shape[1] + 16) * U * (a.abs() @ wd.abs().T)
+    d = ea @ wd.abs().T + _sum_err(a, wd.T, dtype)
     return d + r * ((a @ wd.T).abs() + d)
 
 
 def ffn_grad_bound(x, wg, wu, wd, gy, act, dtype):
     r = HALF_STEP[dtype]
     x, wg, wu, wd, gy = (t.double() for t in (x, wg, wu, wd, gy))
-    T, C = x.shape
     F = wg.shape[0]
     # a may come from the unrounded or from the stored g and u: the larger bound
     g, u, h, dh, eu, eh, edh = _inner(x, wg, wu, act, dtype, True)
@@ -142,19 +155,18 @@ def ffn_grad_bound(x, wg, wu, wd, gy, act, dtype):
     ea = eh * (u.abs() + eu) + h.abs() * eu
     ea = ea + (r + 2 * U) * (a.abs() + ea)
     da = gy @ wd
-    eda = (C + 16) * U * (gy.abs() @ wd.abs())
+    eda = _sum_err(gy, wd, dtype)
     dg, du = da * u * dh, da * h
     edu = eda * (h.abs() + eh) + da.abs() * eh
     edu = edu + (r + 2 * U) * (du.abs() + edu)
     edg = eda * ((u.abs() + eu) * (dh.abs() + edh)) + da.abs() * (eu * (dh.abs() + edh)
                                                                   + u.abs() * edh)
     edg = edg + (r + 3 * U) * (dg.abs() + edg)
-    k2 = (2 * F + 16) * U
-    ex = edg @ wg.abs() + edu @ wu.abs() + k2 * (dg.abs() @ wg.abs() + du.abs() @ wu.abs())
-    kt = (T + 16) * U
-    egw = edg.T @ x.abs() + kt * (dg.abs().T @ x.abs())
-    euw = edu.T @ x.abs() + kt * (du.abs().T @ x.abs())
-    edw = gy.abs().T @ ea + kt * (gy.abs().T @ a.abs())
+    ex = (edg @ wg.abs() + edu @ wu.abs() + _sum_err(dg, wg, dtype, 2 * F)
+          + _sum_err(du, wu, dtype, 2 * F))
+    egw = edg.T @ x.abs() + _sum_err(dg.T, x, dtype)
+    euw = edu.T @ x.abs() + _sum_err(du.T, x, dtype)
+    edw = gy.abs().T @ ea + _sum_err(gy.T, a, dtype)
     outs = (dg @ wg + du @ wu, dg.T @ x, du.T @ x, gy.T @ a)
     return tuple(e + r * (o.abs() + e) for e, o in zip((ex, egw, euw, edw), outs))
 

@@ -212,28 +212,109 @@ def test_gradients_against_differences(mhc, act):
         assert abs(got - want) <= 2e-4 * float(gy.norm()) * float(y.norm()), GRADS[i]
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("T,C,F", [(300, 264, 520), (40, 264, 520), (1500, 1032, 2056)])
 @pytest.mark.parametrize("backward", [False, True])
-def test_times_out_then_recovers(mhc, T, C, F, backward):
+def test_times_out_then_recovers(mhc, T, C, F, backward, dtype):
     """A wait limit of 1 ns makes the kernels' waits give up: the status word says so, and an
     ordinary call on the same buffers and workspace is right again."""
-    x, wg, wu, wd, gy = _case(T, C, F, BF16, 12)
+    x, wg, wu, wd, gy = _case(T, C, F, dtype, 12)
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
     if backward:
-        ws = torch.empty(mhc.mhc_ffn_backward_workspace_size(T, C, F, BF16), dtype=torch.uint8,
+        ws = torch.empty(mhc.mhc_ffn_backward_workspace_size(T, C, F, dtype), dtype=torch.uint8,
                          device="cuda")
         mhc.mhc_ffn_backward(x, wg, wu, wd, gy, workspace=ws, dev_status=st, wait_ns=1)
         assert int(st.item()) == TIMEOUT
         st.zero_()
         got = mhc.mhc_ffn_backward(x, wg, wu, wd, gy, workspace=ws, dev_status=st)
         assert int(st.item()) == 0
-        _check_bwd(got, x, wg, wu, wd, gy, "silu", BF16)
+        _check_bwd(got, x, wg, wu, wd, gy, "silu", dtype)
     else:
-        ws = torch.empty(mhc.mhc_ffn_workspace_size(T, C, F, BF16), dtype=torch.uint8,
+        ws = torch.empty(mhc.mhc_ffn_workspace_size(T, C, F, dtype), dtype=torch.uint8,
                          device="cuda")
         mhc.mhc_ffn(x, wg, wu, wd, workspace=ws, dev_status=st, wait_ns=1)
         assert int(st.item()) == TIMEOUT
         st.zero_()
         y = mhc.mhc_ffn(x, wg, wu, wd, workspace=ws, dev_status=st)
         assert int(st.item()) == 0
-        _check_fwd(y, x, wg, wu, wd, "silu", BF16)
+        _check_fwd(y, x, wg, wu, wd, "silu", dtype)
+
+
+@pytest.mark.parametrize("T", [3, 40, 300])
+def test_powers_of_two_pass_through(mhc, T):
+    """fp32: x scaled by 2^-90 and both projections by 2^90 give the very bits of the unscaled
+    call (all parts of the split operands are still normal numbers)."""
+    x, wg, wu, wd, gy = _case(T, 136, 200, F32, 13)
+    want = mhc.mhc_ffn(x, wg, wu, wd), *mhc.mhc_ffn_backward(x, wg, wu, wd, gy)
+    s = 2.0 ** 90
+    y = mhc.mhc_ffn(x / s, wg * s, wu * s, wd)
+    gx, gwg, gwu, gwd = mhc.mhc_ffn_backward(x / s, wg * s, wu * s, wd, gy)
+    for a, b in zip(want, (y, gx / s, gwg * s, gwu * s, gwd)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T", [4, 100, 300])
+def test_values_near_the_type_limit(mhc, T, dtype):
+    """A token of 3.3e38 with weights that bring it back: finite, and right."""
+    x, wg, wu, wd, _ = _case(T, 64, 72, dtype, 14)
+    x[1] = 0
+    x[1, 3] = 3.3e38
+    wg[:, 3] *= 1e-38
+    wu[:, 3] *= 1e-38
+    _check_fwd(mhc.mhc_ffn(x, wg, wu, wd), x, wg, wu, wd, "silu", dtype)
+
+
+def test_calls_on_two_streams_at_once(mhc):
+    """Independent calls, each with its own workspace, in flight together."""
+    cases = [_case(T, 520, 1032, dt, 20 + i)
+             for i, (T, dt) in enumerate([(3, BF16), (200, BF16), (700, BF16), (5, F32),
+                                          (90, F32), (400, F32)])]
+    want = [(mhc.mhc_ffn(*c[:4]), *mhc.mhc_ffn_backward(*c)) for c in cases]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        got.append([(mhc.mhc_ffn(*c[:4], stream=streams[i % 3]),
+                     *mhc.mhc_ffn_backward(*c, stream=streams[(i + 1) % 3]))
+                    for i, c in enumerate(cases)])
+    torch.cuda.synchronize()
+    for g in got:
+        for a, b in zip(want, g):
+            assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_back_to_back_calls_share_a_workspace(mhc):
+    """Calls on one stream with one workspace: each starts when the one before is done with it,
+    although their kernels are set up early."""
+    a, b = _case(300, 520, 1032, BF16, 30), _case(130, 520, 1032, BF16, 31)
+    want = [[mhc.mhc_ffn(*c[:4]), *mhc.mhc_ffn_backward(*c)] for c in (a, b)]
+    n = max(mhc.mhc_ffn_backward_workspace_size(300, 520, 1032, BF16),
+            mhc.mhc_ffn_workspace_size(300, 520, 1032, BF16))
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    for _ in range(5):
+        got = [[mhc.mhc_ffn(*c[:4], workspace=ws), *mhc.mhc_ffn_backward(*c, workspace=ws)]
+               for c in (a, b)]
+        for w, g in zip(want, got):
+            assert all(torch.equal(p, q) for p, q in zip(w, g))
+
+
+@pytest.mark.slow
+def test_largest_offsets(mhc):
+    """More than 2^31 hidden values: the last tokens agree with the same tokens alone."""
+    T, C, F = 70000, 64, 32768
+    if torch.cuda.get_device_properties(0).total_memory < 100 << 30:
+        pytest.skip("needs 50 GB")
+    x, wg, wu, wd, gy = _case(T, C, F, BF16, 15)
+    y = mhc.mhc_ffn(x, wg, wu, wd)
+    gx, gwg, _, gwd = mhc.mhc_ffn_backward(x, wg, wu, wd, gy)
+    for sl in (slice(0, 64), slice(T - 64, T)):
+        R.assert_within(y[sl], R.ffn(x[sl], wg, wu, wd, "silu"),
+                        R.ffn_bound(x[sl], wg, wu, wd, "silu", BF16), "y")
+        R.assert_within(gx[sl], R.ffn_grad(x[sl], wg, wu, wd, gy[sl], "silu")[0],
+                        R.ffn_grad_bound(x[sl], wg, wu, wd, gy[sl], "silu", BF16)[0], "grad_x")
+    del y, gx
+    # the weight gradients of 32 hidden units, over all tokens
+    f = slice(F - 32, F)
+    ref = R.ffn_grad(x, wg[f], wu[f], wd[:, f], gy, "silu")
+    assert R.norm_rel(gwg[f], ref[1]) < 2.0 ** -7 and R.norm_rel(gwd[:, f], ref[3]) < 2.0 ** -7
