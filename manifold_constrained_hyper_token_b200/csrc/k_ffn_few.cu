@@ -44,6 +44,7 @@ struct FewP {
   __nv_bfloat16 *o0, *o1;
   float *g, *u;          // GATE: kept unless null; DGATE: read
   int act;
+  bool early;            // a later kernel of its call: the weights may be read at once
   uint32_t tmem_cols, acc1;  // columns to allocate; the second accumulator's column
   int* status;
   uint64_t wait_ns;
@@ -98,19 +99,42 @@ __global__ void __launch_bounds__(few::NT) k_ffn_few(const __grid_constant__ Few
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  tc::grid_wait();
-  tc::grid_release();
-
   auto give_up = [&]() {
     *abort_flag = 1;
     flag_status(P.status, MHC_ERR_TIMEOUT);
   };
 
-  if (warp == 0 && lane == 0) {
+  const bool loader = warp == 0 && lane == 0;
+  const uint64_t stream = tc::policy_evict_first(), keep = tc::policy_evict_last();
+  auto load_weights = [&](int it) {
+    const int s = it % P.stages, j = j0 + it, seg = j / P.kblocks;
+    const int k0 = (j - seg * P.kblocks) * TK;
+    const uint32_t base = tc::smem_u32(smem + s * stage_bytes);
+    tc::mbar_arrive_expect_tx(full(s), stage_bytes);
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      const CUtensorMap* m = &P.w[NW == 2 ? i : seg];
+      const uint32_t dst = base + i * WBYTES;
+      if (MN) {
+        tc::tma_load_2d(dst, m, full(s), (int)row0, k0, stream);
+        tc::tma_load_2d(dst + WBYTES / 2, m, full(s), (int)row0 + 64, k0, stream);
+      } else {
+        tc::tma_load_2d(dst, m, full(s), k0, (int)row0, stream);
+      }
+    }
+  };
+  // a ring of weights is on its way while the kernel before this one ends
+  const int blocks = j1 - j0;
+  const int ahead = !P.early ? 0 : blocks < P.stages ? blocks : P.stages;
+  if (loader)
+    for (int it = 0; it < ahead; ++it) load_weights(it);
+  tc::grid_wait();
+  tc::grid_release();
+
+  if (loader) {
     // ---------------------------------------------------------------- TMA
-    const uint64_t stream = tc::policy_evict_first(), keep = tc::policy_evict_last();
     int it = 0;
-    for (int j = j0; j < j1; ++j, ++it) {
+    for (; it < blocks; ++it) {
       const int s = it % P.stages;
       if (it >= P.stages &&
           !tc::mbar_pipe_wait<false>(empty(s), ((uint32_t)(it / P.stages) & 1u) ^ 1u, abort_flag,
@@ -118,21 +142,10 @@ __global__ void __launch_bounds__(few::NT) k_ffn_few(const __grid_constant__ Few
         give_up();
         break;
       }
-      const uint32_t base = tc::smem_u32(smem + s * stage_bytes);
-      const int seg = j / P.kblocks, k0 = (j - seg * P.kblocks) * TK;
-      tc::mbar_arrive_expect_tx(full(s), stage_bytes);
-#pragma unroll
-      for (int i = 0; i < NW; ++i) {
-        const CUtensorMap* m = &P.w[NW == 2 ? i : seg];
-        const uint32_t dst = base + i * WBYTES;
-        if (MN) {
-          tc::tma_load_2d(dst, m, full(s), (int)row0, k0, stream);
-          tc::tma_load_2d(dst + WBYTES / 2, m, full(s), (int)row0 + 64, k0, stream);
-        } else {
-          tc::tma_load_2d(dst, m, full(s), k0, (int)row0, stream);
-        }
-      }
-      tc::tma_load_3d(base + NW * WBYTES, &P.x, full(s), k0, 0, NW == 2 ? 0 : seg, keep);
+      if (it >= ahead) load_weights(it);
+      const int j = j0 + it, seg = j / P.kblocks, k0 = (j - seg * P.kblocks) * TK;
+      tc::tma_load_3d(tc::smem_u32(smem + s * stage_bytes) + NW * WBYTES, &P.x, full(s), k0, 0,
+                      NW == 2 ? 0 : seg, keep);
     }
     // every copy issued here has landed before the CTA can exit
     for (int i = it > P.stages ? it - P.stages : 0; i < it; ++i)
@@ -351,6 +364,7 @@ cudaError_t few_gate(const FewArgs& f, void* a, float* g, float* u, cudaStream_t
 
 cudaError_t few_down(const FewArgs& f, const void* a, void* y, cudaStream_t s) {
   FewP P = base(f, f.C, 1);
+  P.early = true;
   TRY(weight_map(&P.w[0], f.wd, f.C, f.F, false));
   TRY(token_map(&P.x, a, f.t, f.F, 1, P.np));
   P.o0 = (bf16*)y;
@@ -359,6 +373,7 @@ cudaError_t few_down(const FewArgs& f, const void* a, void* y, cudaStream_t s) {
 
 cudaError_t few_dgate(const FewArgs& f, const float* g, const float* u, void* d, cudaStream_t s) {
   FewP P = base(f, f.F, 1);
+  P.early = true;
   TRY(weight_map(&P.w[0], f.wd, f.C, f.F, true));
   TRY(token_map(&P.x, f.gy, f.t, f.C, 1, P.np));
   P.o0 = (bf16*)d;
@@ -370,6 +385,7 @@ cudaError_t few_dgate(const FewArgs& f, const float* g, const float* u, void* d,
 
 cudaError_t few_grad_x(const FewArgs& f, const void* d, void* gx, cudaStream_t s) {
   FewP P = base(f, f.C, 2);
+  P.early = true;
   TRY(weight_map(&P.w[0], f.wg, f.F, f.C, true));
   TRY(weight_map(&P.w[1], f.wu, f.F, f.C, true));
   TRY(token_map(&P.x, d, f.t, f.F, 2, P.np));

@@ -54,6 +54,7 @@ struct Few32P {
   void* o0;                // STORE: fp32 [t][rows]; else bf16 planes [3 or 6][t][rows]
   float *g, *u;            // GATE: kept unless null; DGATE: read
   int act;
+  bool early;              // a later kernel of its call: the weights may be read at once
   uint32_t tmem_cols;      // columns to allocate; an accumulator has np
   int* status;
   uint64_t wait_ns;
@@ -122,13 +123,16 @@ __global__ void __launch_bounds__(few32::NT, 1) k_ffn_few32(const __grid_constan
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  tc::grid_wait();
-  tc::grid_release();
-
   auto give_up = [&]() {
     *abort_flag = 1;
     flag_status(P.status, MHC_ERR_TIMEOUT);
   };
+
+  // the weights' loader needs nothing from the kernel before this one
+  if (warp != 0 || !P.early) {
+    tc::grid_wait();
+    tc::grid_release();
+  }
 
   if (warp == 0) {
     // ------------------------------------------------------- weights, as they are
@@ -162,6 +166,8 @@ __global__ void __launch_bounds__(few32::NT, 1) k_ffn_few32(const __grid_constan
         tc::mbar_wait(raw_full(i % P.raws), (uint32_t)(i / P.raws) & 1u, nullptr,
                       tc::kDrainWaitNs);
     }
+    __syncwarp();
+    if (P.early) tc::grid_wait();  // before the reduction reads g and u
   } else if (warp == 2) {
     // ------------------------------------------------------------ tokens' planes
     if (lane == 0) {
@@ -471,6 +477,7 @@ cudaError_t few32_gate(const FewArgs& f, void* a, float* g, float* u, cudaStream
 
 cudaError_t few32_down(const FewArgs& f, const void* a, float* y, cudaStream_t s) {
   Few32P P = base(f, f.C, 1);
+  P.early = true;
   TRY(weight_map(&P.w[0], f.wd, f.C, f.F, false));
   TRY(token_map(&P.x, a, f.t, f.F, 3, P.np));
   P.o0 = y;
@@ -479,6 +486,7 @@ cudaError_t few32_down(const FewArgs& f, const void* a, float* y, cudaStream_t s
 
 cudaError_t few32_dgate(const FewArgs& f, const float* g, const float* u, void* d, cudaStream_t s) {
   Few32P P = base(f, f.F, 1);
+  P.early = true;
   TRY(weight_map(&P.w[0], f.wd, f.C, f.F, true));
   TRY(token_map(&P.x, f.gy, f.t, f.C, 3, P.np));
   P.o0 = d;
@@ -489,6 +497,7 @@ cudaError_t few32_dgate(const FewArgs& f, const float* g, const float* u, void* 
 
 cudaError_t few32_grad_x(const FewArgs& f, const void* d, float* gx, cudaStream_t s) {
   Few32P P = base(f, f.C, 2);
+  P.early = true;
   TRY(weight_map(&P.w[0], f.wg, f.F, f.C, true));
   TRY(weight_map(&P.w[1], f.wu, f.F, f.C, true));
   TRY(token_map(&P.x, d, f.t, f.F, 6, P.np));

@@ -34,6 +34,7 @@ struct OneP {
   __nv_bfloat16* planes;       // GATE, DGATE: the planes of a, or of dg and du; may be null
   float *g, *u;                // GATE: kept unless null; DGATE: read
   int act;
+  bool early;                  // a later kernel of its call: weights may be read at once
 };
 
 __device__ __forceinline__ float4 ld_once(const float* p) {
@@ -100,8 +101,6 @@ __global__ void __launch_bounds__(NTHR) k_rows(const __grid_constant__ OneP P) {
   const int64_t row0 = (int64_t)(blockIdx.x / P.parts) * TILE;
   const int64_t chunks = (P.K + RCHUNK - 1) / RCHUNK;
   const int64_t c0 = chunks * rank / P.parts, c1 = chunks * (rank + 1) / P.parts;
-  tc::grid_wait();
-  tc::grid_release();
   // this warp's rows; past the end the last one again (not stored)
   const float* wr[RPW];
 #pragma unroll
@@ -131,8 +130,11 @@ __global__ void __launch_bounds__(NTHR) k_rows(const __grid_constant__ OneP P) {
   };
   float acc[RPW][TT] = {};
   float4 next[2][RPW];
+  if (P.early && c0 < c1) fetch(c0, next);
+  tc::grid_wait();
+  tc::grid_release();
   if (c0 < c1) {
-    fetch(c0, next);
+    if (!P.early) fetch(c0, next);
     stage(c0, 0);
   }
   __syncthreads();
@@ -207,8 +209,6 @@ __global__ void __launch_bounds__(NTHR) k_cols(const __grid_constant__ OneP P) {
   const int64_t row0 = (int64_t)(blockIdx.x / P.parts) * CTILE, row = row0 + 4 * lane;
   const int64_t per = (P.K + CCHUNK - 1) / CCHUNK, chunks = per * P.nseg;
   const int64_t c0 = chunks * rank / P.parts, c1 = chunks * (rank + 1) / P.parts;
-  tc::grid_wait();
-  tc::grid_release();
   auto stage = [&](int64_t c, int b) {
     const int64_t seg = c / per, kb = (c - seg * per) * CCHUNK;
     const float* x = P.x + seg * P.t * P.K;
@@ -230,8 +230,11 @@ __global__ void __launch_bounds__(NTHR) k_cols(const __grid_constant__ OneP P) {
   };
   float acc[TT][4] = {};
   float4 next[8];
+  if (P.early && c0 < c1) fetch(c0, next);
+  tc::grid_wait();
+  tc::grid_release();
   if (c0 < c1) {
-    fetch(c0, next);
+    if (!P.early) fetch(c0, next);
     stage(c0, 0);
   }
   __syncthreads();
@@ -341,25 +344,27 @@ template <OneEpi E> cudaError_t cols(OneP& P, cudaStream_t s) {
 cudaError_t one32_gate(const FewArgs& f, float* a, void* planes, float* g, float* u,
                        cudaStream_t s) {
   OneP P{{(const float*)f.wg, (const float*)f.wu}, (const float*)f.x, f.C, f.F, f.t, 1, 1, a,
-         (__nv_bfloat16*)planes, g, u, f.act};
+         (__nv_bfloat16*)planes, g, u, f.act, false};
   return rows<ONE_GATE>(P, s);
 }
 
 cudaError_t one32_down(const FewArgs& f, const float* a, float* y, cudaStream_t s) {
-  OneP P{{(const float*)f.wd, nullptr}, a, f.F, f.C, f.t, 1, 1, y, nullptr, nullptr, nullptr, 0};
+  OneP P{{(const float*)f.wd, nullptr}, a, f.F, f.C, f.t, 1, 1, y, nullptr, nullptr, nullptr, 0,
+         true};
   return rows<ONE_STORE>(P, s);
 }
 
 cudaError_t one32_dgate(const FewArgs& f, const float* g, const float* u, float* d, void* planes,
                         cudaStream_t s) {
   OneP P{{(const float*)f.wd, nullptr}, (const float*)f.gy, f.C, f.F, f.t, 1, 1, d,
-         (__nv_bfloat16*)planes, const_cast<float*>(g), const_cast<float*>(u), f.act};
+         (__nv_bfloat16*)planes, const_cast<float*>(g), const_cast<float*>(u), f.act,
+         true};
   return cols<ONE_DGATE>(P, s);
 }
 
 cudaError_t one32_grad_x(const FewArgs& f, const float* d, float* gx, cudaStream_t s) {
   OneP P{{(const float*)f.wg, (const float*)f.wu}, d, f.F, f.C, f.t, 2, 1, gx, nullptr, nullptr,
-         nullptr, 0};
+         nullptr, 0, true};
   return cols<ONE_STORE>(P, s);
 }
 

@@ -24,7 +24,8 @@ __device__ __forceinline__ void cluster_sync() {
 // finished (and so has all that it waited for itself).  A kernel that releases
 // after its wait lets the next one run beside it: a next kernel that needs nothing
 // from it may work at once and call grid_wait last, before it ends, so that the
-// end of a kernel still means the end of all before it.
+// end of a kernel still means the end of all before it.  In particular the second
+// and later kernels of a call may read the call's inputs before their grid_wait.
 __device__ __forceinline__ void grid_release() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
