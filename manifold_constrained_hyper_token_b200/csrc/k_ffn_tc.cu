@@ -3,8 +3,9 @@
 //
 //   D[m][n] = sum_k A(m, k) B(n, k)
 //
-// with either operand stored along k or along its own rows, and four epilogues:
+// with either operand stored along k or along its own rows, and five epilogues:
 //   EPI_STORE  D itself
+//   EPI_PART   D's fp32 sums over a part of k (k_join adds the parts)
 //   EPI_GATE   two products at once (A = x, B = w_gate and w_up): act(g) u
 //   EPI_KEEP   the same, and g and u themselves (the backward's recompute)
 //   EPI_DGATE  D = da: reads g and u, writes dg = da u act'(g), du = da act(g)
@@ -76,7 +77,7 @@ template <int TN, bool F32> struct Cfg {
 
 namespace {
 
-enum Epi { EPI_STORE, EPI_GATE, EPI_KEEP, EPI_DGATE };
+enum Epi { EPI_STORE, EPI_GATE, EPI_KEEP, EPI_DGATE, EPI_PART };
 
 // One launch: the sum of nseg products into each tile, the s-th of A's planes
 // from s NP on by B's map s.
@@ -85,6 +86,7 @@ struct GemmArgs {
   int nseg, kblocks;
   int mt, nt, nz;         // tiles of a problem; problems (planes of A and a map of D each)
   int zplanes;            // planes of A per problem
+  int split;              // PART: parts of k; part q of problem z goes to plane z split + q
   int64_t M, N;           // rows and columns of D (columns of one product for GATE, KEEP)
   const float *g, *u;     // EPI_DGATE
   int act;
@@ -93,17 +95,23 @@ struct GemmArgs {
   uint64_t wait_ns;
 };
 
-// The k blocks of the stay in an accumulator that starts at k block j0 end here.
-template <bool F32> __device__ __forceinline__ int stay_end(int j0, int nk) {
-  return !F32 || nk - j0 < ftc::kChunk ? nk : j0 + ftc::kChunk;
+// The stay in an accumulator that starts at k block j0 of a tile that ends at jb
+// ends here.
+template <bool F32> __device__ __forceinline__ int stay_end(int j0, int jb) {
+  return !F32 || jb - j0 < ftc::kChunk ? jb : j0 + ftc::kChunk;
 }
 
-// A tile's place: problem z, row tile, column tile; bands of BAND row tiles, row
-// tiles fastest.
-__device__ __forceinline__ void tile_at(const GemmArgs& P, int64_t id, int& z, int& mi, int& ni) {
-  const int64_t per = (int64_t)P.mt * P.nt;
+// A tile's place: plane z of the results (problem z / split, part z % split), row
+// tile, column tile, and its k blocks [ja, jb); bands of BAND row tiles, row tiles
+// fastest.
+__device__ __forceinline__ void tile_at(const GemmArgs& P, int64_t id, int& z, int& mi, int& ni,
+                                        int& ja, int& jb) {
+  const int64_t per = (int64_t)P.mt * P.nt, nk = (int64_t)P.nseg * P.kblocks;
   z = (int)(id / per);
   id -= (int64_t)z * per;
+  const int q = z % P.split;
+  ja = (int)(nk * q / P.split);
+  jb = (int)(nk * (q + 1) / P.split);
   const int64_t band = id / ((int64_t)ftc::BAND * P.nt);
   const int m0 = (int)band * ftc::BAND;
   const int rows = P.mt - m0 < ftc::BAND ? P.mt - m0 : ftc::BAND;
@@ -212,7 +220,7 @@ __global__ void __launch_bounds__(ftc::NT, 1)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int rank = (int)tc::cluster_rank();
   const int64_t pair = blockIdx.x / 2, npairs = gridDim.x / 2;
-  const int64_t tiles = (int64_t)P.mt * P.nt * P.nz;
+  const int64_t tiles = (int64_t)P.mt * P.nt * P.nz * P.split;
   constexpr bool DUAL = E == EPI_GATE || E == EPI_KEEP;
 
   if (threadIdx.x == 0) {
@@ -258,26 +266,29 @@ __global__ void __launch_bounds__(ftc::NT, 1)
       int64_t it = 0;
       bool ok = true;
       for (int64_t id = pair; id < tiles && ok; id += npairs) {
-        int z, mi, ni;
-        tile_at(P, id, z, mi, ni);
+        int z, mi, ni, ja, jb;
+        tile_at(P, id, z, mi, ni, ja, jb);
         const int arow = mi * TM + rank * HALF;
         const int brow = DUAL ? ni * HN : ni * TN + rank * HN;
-        for (int sg = 0; sg < P.nseg && ok; ++sg) {
-          const CUtensorMap* bm = &P.b[DUAL ? rank : sg];
-          const int ap = sg * G::NP + z * P.zplanes;
-          for (int kb = 0; kb < P.kblocks; ++kb, ++it) {
-            const int s = (int)(it % NS);
-            if (it >= NS && !tc::mbar_pipe_wait<false>(empty(s), ((uint32_t)(it / NS) & 1u) ^ 1u,
-                                                       abort_flag, P.wait_ns)) {
-              give_up();
-              ok = false;
-              break;
-            }
-            const uint32_t base = tc::smem_u32(smem + s * STAGE);
-            if (rank == 0) tc::mbar_arrive_expect_tx(full(s), 2 * STAGE);
-            const uint32_t bar = tc::map_cta(full(s), 0);
-            load_rows<G, HALF, AMN>(base, &P.a, bar, arow, kb * TK, ap, pol);
-            load_rows<G, HN, BMN>(base + G::ABYTES, bm, bar, brow, kb * TK, 0, pol);
+        const int zplane = z / P.split * P.zplanes;
+        int seg = ja / P.kblocks, kb = ja - seg * P.kblocks;
+        for (int j = ja; j < jb; ++j, ++it) {
+          const int s = (int)(it % NS);
+          if (it >= NS && !tc::mbar_pipe_wait<false>(empty(s), ((uint32_t)(it / NS) & 1u) ^ 1u,
+                                                     abort_flag, P.wait_ns)) {
+            give_up();
+            ok = false;
+            break;
+          }
+          const uint32_t base = tc::smem_u32(smem + s * STAGE);
+          if (rank == 0) tc::mbar_arrive_expect_tx(full(s), 2 * STAGE);
+          const uint32_t bar = tc::map_cta(full(s), 0);
+          load_rows<G, HALF, AMN>(base, &P.a, bar, arow, kb * TK, seg * G::NP + zplane, pol);
+          load_rows<G, HN, BMN>(base + G::ABYTES, &P.b[DUAL ? rank : seg], bar, brow, kb * TK, 0,
+                                pol);
+          if (++kb == P.kblocks) {
+            kb = 0;
+            ++seg;
           }
         }
       }
@@ -300,7 +311,6 @@ __global__ void __launch_bounds__(ftc::NT, 1)
     // ---------------------------------------------------------------- MMA
     if (lane == 0 && rank == 0) {
       constexpr uint32_t idesc = tc::idesc_bf16(TM, TN, AMN, BMN);
-      const int nk = P.nseg * P.kblocks;
       int64_t it = 0;
       int n = 0;  // accumulators filled so far
       bool ok = true, any = false;
@@ -311,8 +321,10 @@ __global__ void __launch_bounds__(ftc::NT, 1)
           give_up();
           break;
         }
-        for (int j0 = 0, j1; j0 < nk && ok; j0 = j1, ++n) {
-          j1 = stay_end<F32>(j0, nk);
+        int z, mi, ni, ja, jb;
+        tile_at(P, id, z, mi, ni, ja, jb);
+        for (int j0 = ja, j1; j0 < jb && ok; j0 = j1, ++n) {
+          j1 = stay_end<F32>(j0, jb);
           const int buf = n & 1;
           if (n >= 2 && !tc::mbar_pipe_wait<true>(tempty(buf), ((uint32_t)(n / 2) & 1u) ^ 1u,
                                                   abort_flag, P.wait_ns)) {
@@ -338,7 +350,7 @@ __global__ void __launch_bounds__(ftc::NT, 1)
 #pragma unroll
             for (int k = 0; k < TK / 16; ++k) {
               if (F32) {
-                mma(G::MINOR, 2, 0, k, j > 0 || k > 0);
+                mma(G::MINOR, 2, 0, k, j > ja || k > 0);
                 mma(G::MINOR, 1, 1, k, true);
                 mma(G::MINOR, 0, 2, k, true);
                 mma(G::MINOR, 1, 0, k, true);
@@ -365,7 +377,8 @@ __global__ void __launch_bounds__(ftc::NT, 1)
     // first pass over the code is a pass through instruction-cache misses.
     constexpr int NB = F32 ? 3 : 1;                // boxes of one operand
     constexpr bool WIDE = E == EPI_STORE && !F32;  // plain bf16: 64 columns at a time
-    constexpr int SET = E == EPI_STORE  ? 2 * BOX
+    constexpr bool PLAIN = E == EPI_STORE || E == EPI_PART;
+    constexpr int SET = PLAIN           ? 2 * BOX
                         : E == EPI_GATE ? NB * BOX
                         : E == EPI_KEEP ? (2 + NB) * BOX
                                         : 2 * NB * BOX;
@@ -374,18 +387,17 @@ __global__ void __launch_bounds__(ftc::NT, 1)
     constexpr int COLS = DUAL ? HN : TN;  // columns of D's tile
     const int q = warp & 3;               // TMEM lane quarter this warp may read
     uint8_t* out = smem + G::OUT_OFF + q * G::OUT;
-    const int nk = P.nseg * P.kblocks;
     const uint32_t sums = tmem + ((uint32_t)(32 * q) << 16) + G::SUMS;
     // a tile's products may rightly take longer than one wait: 4 us per k block more
-    const uint64_t tile_ns = P.wait_ns + (uint64_t)nk * 4000;
+    const uint64_t tile_ns = P.wait_ns + (uint64_t)P.nseg * P.kblocks * 4000;
     int n = 0, nset = 0;
     for (int64_t id = pair; id < tiles; id += npairs) {
-      int z, mi, ni;
-      tile_at(P, id, z, mi, ni);
+      int z, mi, ni, ja, jb;
+      tile_at(P, id, z, mi, ni, ja, jb);
       const int64_t row0 = (int64_t)mi * TM + rank * HALF + 32 * q, row = row0 + lane;
       bool ok = true;
-      for (int j0 = 0, j1; j0 < nk; j0 = j1, ++n) {
-        j1 = stay_end<F32>(j0, nk);
+      for (int j0 = ja, j1; j0 < jb; j0 = j1, ++n) {
+        j1 = stay_end<F32>(j0, jb);
         const int buf = n & 1;
         ok = tc::mbar_pipe_wait<false>(tfull(buf), (uint32_t)(n / 2) & 1u, abort_flag, tile_ns);
         if (!ok && !*abort_flag) give_up();
@@ -398,14 +410,14 @@ __global__ void __launch_bounds__(ftc::NT, 1)
 #pragma unroll 1
           for (int c = 0; c < TN; c += 16) {
             float v[16], m[16];
-            if (j0 == 0) {
+            if (j0 == ja) {
               tc::tmem_get16(ta + c, v);
             } else {
               tc::tmem_get16x2(ta + c, sums + c, v, m);
 #pragma unroll
               for (int i = 0; i < 16; ++i) v[i] += m[i];
             }
-            if (j1 == nk) {
+            if (j1 == jb) {
               tc::tmem_get16(sums + c - G::SUMS + G::MINOR, m);
 #pragma unroll
               for (int i = 0; i < 16; ++i) v[i] += m[i];
@@ -416,10 +428,10 @@ __global__ void __launch_bounds__(ftc::NT, 1)
           __syncwarp();
           if (lane == 0) {
             tc::mbar_arrive_cluster(tc::map_cta(tempty(buf), 0));
-            if (j1 == nk) tc::mbar_arrive_cluster(tc::map_cta(mempty, 0));
+            if (j1 == jb) tc::mbar_arrive_cluster(tc::map_cta(mempty, 0));
           }
         }
-        if (j1 == nk) {
+        if (j1 == jb) {
           const uint32_t at = F32 ? sums : ta;  // D's columns
 #pragma unroll 1
           for (int c = 0; c < COLS; c += WIDE ? 64 : 32) {
@@ -442,7 +454,7 @@ __global__ void __launch_bounds__(ftc::NT, 1)
                   *reinterpret_cast<uint4*>(box + lane * 128 + (((4 * g + p) ^ (lane & 7)) << 4)) =
                       make_uint4(bf2(w[8 * p], w[8 * p + 1]), bf2(w[8 * p + 2], w[8 * p + 3]),
                                  bf2(w[8 * p + 4], w[8 * p + 5]), bf2(w[8 * p + 6], w[8 * p + 7]));
-              } else if (E == EPI_STORE) {
+              } else if (PLAIN) {
                 tc::tmem_get16(at + cg, v);
                 put_f32(box + g * BOX, lane, v);
               } else if (DUAL) {
@@ -493,9 +505,11 @@ __global__ void __launch_bounds__(ftc::NT, 1)
               if (in) {
                 if (WIDE) {
                   tc::tma_store_3d(&P.d[z], bu, cc, rr, 0);
-                } else if (E == EPI_STORE) {
-                  tc::tma_store_3d(&P.d[z], bu, cc, rr, 0);
-                  if (col + 16 < P.N) tc::tma_store_3d(&P.d[z], bu + BOX, cc + 16, rr, 0);
+                } else if (PLAIN) {
+                  const CUtensorMap* d = &P.d[E == EPI_PART ? 0 : z];
+                  const int plane = E == EPI_PART ? z : 0;
+                  tc::tma_store_3d(d, bu, cc, rr, plane);
+                  if (col + 16 < P.N) tc::tma_store_3d(d, bu + BOX, cc + 16, rr, plane);
                 } else if (E == EPI_DGATE) {
                   for (int pl = 0; pl < 2 * NB; ++pl)
                     tc::tma_store_3d(&P.d[0], bu + pl * BOX, cc, rr, pl);
@@ -554,6 +568,36 @@ __global__ void __launch_bounds__(256) k_split3(const __grid_constant__ SplitArg
       for (int pl = 0; pl < 3; ++pl)
         *reinterpret_cast<uint4*>(a.dst[q] + pl * n + i) =
             make_uint4(p[pl][0].x, p[pl][0].y, p[pl][1].x, p[pl][1].y);
+    }
+  }
+}
+
+// The parts of up to four results, added in order: n elements each, `split` planes
+// of fp32 sums (split == 0: no such result).
+struct JoinArgs {
+  const float* part[4];
+  void* out[4];
+  int64_t n[4];
+  int split[4];
+};
+template <bool F32>
+__global__ void __launch_bounds__(256) k_join(const __grid_constant__ JoinArgs a) {
+  tc::grid_wait();
+  tc::grid_release();
+  for (int q = 0; q < 4; ++q) {
+    if (a.split[q] == 0) continue;
+    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < a.n[q];
+         i += (int64_t)gridDim.x * 256 * 4) {
+      float4 v = __ldcs(reinterpret_cast<const float4*>(a.part[q] + i));
+      for (int k = 1; k < a.split[q]; ++k) {
+        const float4 w = __ldcs(reinterpret_cast<const float4*>(a.part[q] + k * a.n[q] + i));
+        v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+      }
+      if (F32)
+        *reinterpret_cast<float4*>((float*)a.out[q] + i) = v;
+      else
+        *reinterpret_cast<uint2*>((__nv_bfloat16*)a.out[q] + i) =
+            make_uint2(bf2(v.x, v.y), bf2(v.z, v.w));
     }
   }
 }
@@ -624,28 +668,50 @@ cudaError_t launch_tn(GemmArgs& P, const Opnds& o, cudaStream_t s) {
   P.nt = tiles_of(P.N, DUAL ? TN / 2 : TN);
   auto kern = k_ffn_tc<E, AMN, BMN, F32, TN>;
   TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM));
-  const int64_t tiles = (int64_t)P.mt * P.nt * P.nz, pairs = sm_pairs();
+  const int64_t tiles = (int64_t)P.mt * P.nt * P.nz * P.split, pairs = sm_pairs();
   return launch_after(kern, (unsigned)(2 * (tiles < pairs ? tiles : pairs)), ftc::NT, G::SMEM, 2, s,
                       P);
 }
 
-// fp32: 256 x 128 tiles (four TMEM regions).  bf16: 256 x 256, or 256 x 128
-// where its rounds over the pairs come to less: a narrow tile has half the work
-// and takes 0.72 of the time (T = 8192, C = 7168, F = 14336: 5.41 against 3.63 ms
-// for the forward pass).
+// How a product is cut.  fp32: 256 x 128 tiles (four TMEM regions).  bf16: 256 x
+// 256, or 256 x 128 where its rounds over the pairs come to less: a narrow tile has
+// half the work and takes 0.72 of the time (T = 8192, C = 7168, F = 14336: 5.41
+// against 3.63 ms for the forward pass).  A plain result of few tiles and a long k
+// is also split along k, into parts of eight k blocks at least, where that saves 24
+// blocks of about a quarter of a microsecond: adding up the parts costs four.
+struct Plan {
+  int tn, split;
+};
+Plan plan(bool f32, bool dual, bool plain, int64_t M, int64_t N, int nz, int64_t K, int nseg) {
+  constexpr int64_t pairs = 74;  // of 148 SMs; the workspace's size follows from it
+  const int64_t rows = (int64_t)tiles_of(M, ftc::TM) * nz;
+  const int64_t wide = rows * tiles_of(N, dual ? 128 : 256);
+  const int64_t half = rows * tiles_of(N, dual ? 64 : 128);
+  Plan p{256, 1};
+  if (f32 || 72 * ((half + pairs - 1) / pairs) < 100 * ((wide + pairs - 1) / pairs)) p.tn = 128;
+  const int64_t tiles = p.tn == 128 ? half : wide, nk = (int64_t)nseg * tiles_of(K, f32 ? 32 : 64);
+  if (plain && 2 * tiles <= pairs) {
+    const int64_t s = std::min<int64_t>(std::min(pairs / tiles, nk / 8), 16);
+    if (s > 1 && nk - nk / s >= 24) p.split = (int)s;
+  }
+  return p;
+}
+size_t part_bytes(const Plan& p, int64_t M, int64_t N, int nz) {
+  return p.split > 1 ? (size_t)nz * p.split * M * N * 4 : 0;
+}
+
 template <Epi E, bool AMN, bool BMN, bool F32>
-cudaError_t launch(GemmArgs& P, const Opnds& o, cudaStream_t s) {
+cudaError_t launch(GemmArgs& P, const Opnds& o, int tn, cudaStream_t s) {
   if constexpr (F32) {
     return launch_tn<E, AMN, BMN, true, 128>(P, o, s);
   } else {
-    constexpr bool DUAL = E == EPI_GATE || E == EPI_KEEP;
-    const int64_t rows = (int64_t)tiles_of(P.M, ftc::TM) * P.nz, pairs = sm_pairs();
-    const int64_t wide = rows * tiles_of(P.N, DUAL ? 128 : 256);
-    const int64_t half = rows * tiles_of(P.N, DUAL ? 64 : 128);
-    if (72 * ((half + pairs - 1) / pairs) < 100 * ((wide + pairs - 1) / pairs))
-      return launch_tn<E, AMN, BMN, false, 128>(P, o, s);
-    return launch_tn<E, AMN, BMN, false, 256>(P, o, s);
+    return tn == 128 ? launch_tn<E, AMN, BMN, false, 128>(P, o, s)
+                     : launch_tn<E, AMN, BMN, false, 256>(P, o, s);
   }
+}
+
+bool few_tokens(bool f32, int64_t t, int64_t C, int64_t F) {
+  return f32 ? t <= kOneTokens || few32_fits(t, C, F) : t <= kFewTokens;
 }
 
 // Operands as the products take them: the caller's bf16 arrays, or the split
@@ -660,7 +726,7 @@ struct Ffn {
   const void *x32, *gy32;
   bool is_one() const { return np == 3 && t <= kOneTokens; }
   FewArgs one() const { return {t, C, F, act, x32, wg, wu, wd, gy32, st, wait_ns}; }
-  bool is_few() const { return np == 3 ? is_one() || few32_fits(t, C, F) : t <= kFewTokens; }
+  bool is_few() const { return few_tokens(np == 3, t, C, F); }
   FewArgs few() const { return {t, C, F, act, x, wg, wu, wd, gy, st, wait_ns}; }
 };
 
@@ -668,6 +734,7 @@ struct Ffn {
 GemmArgs base_args(const Ffn& f, int pairs, int64_t M, int64_t N) {
   GemmArgs P{};
   P.nz = 1;
+  P.split = 1;
   P.M = M;
   P.N = N;
   P.act = f.act;
@@ -684,13 +751,43 @@ template <bool F32> cudaError_t gate_product(const Ffn& f, void* a, float* g, fl
   const Opnds o{{f.x, f.t, f.C, f.np, false},
                 {{f.wg, f.F, f.C, f.np, false}, {f.wu, f.F, f.C, f.np, false}}, f.C};
   TRY(result_map(&P.d[0], {a, f.t, f.F, f.np, false}, false));
-  if (g == nullptr) return launch<EPI_GATE, false, false, F32>(P, o, s);
+  const int tn = plan(F32, true, false, f.t, f.F, 1, f.C, 1).tn;
+  if (g == nullptr) return launch<EPI_GATE, false, false, F32>(P, o, tn, s);
   TRY(result_map(&P.d[1], {g, f.t, f.F, 1, true}, false));
   TRY(result_map(&P.d[2], {u, f.t, f.F, 1, true}, false));
-  return launch<EPI_KEEP, false, false, F32>(P, o, s);
+  return launch<EPI_KEEP, false, false, F32>(P, o, tn, s);
 }
 
-template <bool F32> cudaError_t fwd(const Ffn& f, void* y, void* a, cudaStream_t s) {
+// The nz plain results of a product, into out[], at once or in parts that k_join
+// adds up (J's next entries).
+template <bool AMN, bool BMN, bool F32>
+cudaError_t plain_product(GemmArgs& P, const Opnds& o, void* const* out, float* part, JoinArgs& J,
+                          int& joins, cudaStream_t s) {
+  const Plan p = plan(F32, false, true, P.M, P.N, P.nz, o.K, P.nseg);
+  if (p.split == 1) {
+    for (int z = 0; z < P.nz; ++z) TRY(result_map(&P.d[z], {out[z], P.M, P.N, 1, F32}, true));
+    return launch<EPI_STORE, AMN, BMN, F32>(P, o, p.tn, s);
+  }
+  P.split = p.split;
+  TRY(result_map(&P.d[0], {part, P.M, P.N, P.nz * p.split, true}, false));
+  for (int z = 0; z < P.nz; ++z, ++joins) {
+    J.part[joins] = part + (int64_t)z * p.split * P.M * P.N;
+    J.out[joins] = out[z];
+    J.n[joins] = P.M * P.N;
+    J.split[joins] = p.split;
+  }
+  return launch<EPI_PART, AMN, BMN, F32>(P, o, p.tn, s);
+}
+template <bool F32> cudaError_t join(const JoinArgs& J, int joins, cudaStream_t s) {
+  if (joins == 0) return cudaSuccess;
+  int64_t most = 0;
+  for (int q = 0; q < joins; ++q) most = std::max(most, J.n[q]);
+  return launch_after(k_join<F32>, (unsigned)std::min<int64_t>((most / 4 + 255) / 256, 592), 256, 0,
+                      1, s, J);
+}
+
+template <bool F32>
+cudaError_t fwd(const Ffn& f, void* y, void* a, float* part, cudaStream_t s) {
   if (f.is_few()) {
     if constexpr (F32) {
       if (f.is_one()) {
@@ -706,15 +803,35 @@ template <bool F32> cudaError_t fwd(const Ffn& f, void* y, void* a, cudaStream_t
   }
   TRY(gate_product<F32>(f, a, nullptr, nullptr, s));
   GemmArgs P = base_args(f, 1, f.t, f.C);
-  TRY(result_map(&P.d[0], {y, f.t, f.C, 1, F32}, true));
-  return launch<EPI_STORE, false, false, F32>(
-      P, {{a, f.t, f.F, f.np, false}, {{f.wd, f.C, f.F, f.np, false}}, f.F}, s);
+  JoinArgs J{};
+  int joins = 0;
+  TRY((plain_product<false, false, F32>(
+      P, {{a, f.t, f.F, f.np, false}, {{f.wd, f.C, f.F, f.np, false}}, f.F}, &y, part, J, joins,
+      s)));
+  return join<F32>(J, joins, s);
+}
+
+// Where the parts of the backward's plain products go (floats from the start).
+struct Parts {
+  size_t gx, gw, gwd, bytes;
+};
+Parts parts_of(bool f32, bool few, int64_t t, int64_t C, int64_t F) {
+  Parts p{};
+  auto take = [&](size_t bytes) {
+    const size_t o = p.bytes / 4;
+    p.bytes += (bytes + 255) / 256 * 256;
+    return o;
+  };
+  p.gx = take(few ? 0 : part_bytes(plan(f32, false, true, t, C, 1, F, 2), t, C, 1));
+  p.gw = take(part_bytes(plan(f32, false, true, F, C, 2, t, 1), F, C, 2));
+  p.gwd = take(part_bytes(plan(f32, false, true, C, F, 1, t, 1), C, F, 1));
+  return p;
 }
 
 // a [np][t][F], d [2 np][t][F] (dg, du), g and u [t][F].
 template <bool F32>
 cudaError_t bwd(const Ffn& f, void* gx, void* gwg, void* gwu, void* gwd, void* a, void* d,
-                float* d32, float* g, float* u, cudaStream_t s) {
+                float* d32, float* g, float* u, float* part, cudaStream_t s) {
   const int np = f.np;
   const Mat X{f.x, f.t, f.C, np, false}, GY{f.gy, f.t, f.C, np, false};
   const Mat A{a, f.t, f.F, np, false}, D{d, f.t, f.F, 2 * np, false};
@@ -736,8 +853,12 @@ cudaError_t bwd(const Ffn& f, void* gx, void* gwg, void* gwu, void* gwd, void* a
     TRY(result_map(&P.d[0], D, false));
     P.g = g;
     P.u = u;
-    TRY((launch<EPI_DGATE, false, true, F32>(P, {GY, {WD}, f.C}, s)));
+    TRY((launch<EPI_DGATE, false, true, F32>(
+        P, {GY, {WD}, f.C}, plan(F32, false, false, f.t, f.F, 1, f.C, 1).tn, s)));
   }
+  const Parts parts = parts_of(F32, few, f.t, f.C, f.F);
+  JoinArgs J{};
+  int joins = 0;
   // the rest needs only what is finished when the next kernel starts: the three
   // run beside one another, each filling the SMs that the one before leaves idle
   if (f.is_one()) {
@@ -748,36 +869,37 @@ cudaError_t bwd(const Ffn& f, void* gx, void* gwg, void* gwu, void* gwd, void* a
     TRY(few_grad_x(f.few(), d, gx, s));
   } else {
     GemmArgs P = base_args(f, 2, f.t, f.C);
-    TRY(result_map(&P.d[0], {gx, f.t, f.C, 1, F32}, true));
-    TRY((launch<EPI_STORE, false, true, F32>(P, {D, {WG, WU}, f.F}, s)));
+    TRY((plain_product<false, true, F32>(P, {D, {WG, WU}, f.F}, &gx, part + parts.gx, J, joins,
+                                         s)));
   }
   {
     GemmArgs P = base_args(f, 1, f.F, f.C);
     P.nz = 2;
     P.zplanes = np;
     P.beside = true;
-    TRY(result_map(&P.d[0], {gwg, f.F, f.C, 1, F32}, true));
-    TRY(result_map(&P.d[1], {gwu, f.F, f.C, 1, F32}, true));
-    TRY((launch<EPI_STORE, true, true, F32>(P, {D, {X}, f.t}, s)));
+    void* const out[2] = {gwg, gwu};
+    TRY((plain_product<true, true, F32>(P, {D, {X}, f.t}, out, part + parts.gw, J, joins, s)));
   }
   GemmArgs P = base_args(f, 1, f.C, f.F);
   P.beside = true;
-  TRY(result_map(&P.d[0], {gwd, f.C, f.F, 1, F32}, true));
-  return launch<EPI_STORE, true, true, F32>(P, {GY, {A}, f.t}, s);
+  TRY((plain_product<true, true, F32>(P, {GY, {A}, f.t}, &gwd, part + parts.gwd, J, joins, s)));
+  return join<F32>(J, joins, s);
 }
 
 size_t up(size_t v) { return (v + 255) / 256 * 256; }
 
 // Workspaces.  The planes of a (one in bf16, three in fp32); with the backward
 // also of dg and du, and g and u in fp32.  fp32: the split copies of the inputs
-// (with few tokens the weights are split on their way into the products).
+// (with few tokens the weights are split on their way into the products).  The
+// parts of products that are split along k.
 struct Layout {
-  size_t a, d, d32, g, u, x, wg, wu, wd, gy, total;
+  size_t a, d, d32, g, u, x, wg, wu, wd, gy, part, total;
 };
 Layout layout(bool f32, bool backward, int64_t t, int64_t C, int64_t F) {
   Layout w{};
   size_t off = 0;
   const size_t np = f32 ? 3 : 1, hid = (size_t)t * F, io = (size_t)t * C, wt = (size_t)F * C;
+  const bool few = few_tokens(f32, t, C, F);
   auto take = [&](size_t bytes) {
     const size_t o = off;
     off = up(off + bytes);
@@ -793,12 +915,15 @@ Layout layout(bool f32, bool backward, int64_t t, int64_t C, int64_t F) {
   if (f32) {
     w.x = take(io * 6);
     if (backward) w.gy = take(io * 6);
-    if (t > kOneTokens && !few32_fits(t, C, F)) {
+    if (!few) {
       w.wg = take(wt * 6);
       w.wu = take(wt * 6);
       w.wd = take(wt * 6);
     }
   }
+  w.part = take(backward ? parts_of(f32, few, t, C, F).bytes
+                : few    ? 0
+                         : part_bytes(plan(f32, false, true, t, C, 1, F, 1), t, C, 1));
   w.total = off;
   return w;
 }
@@ -847,7 +972,8 @@ cudaError_t ffn_fwd_dispatch(int dtype, int act, int64_t t, int64_t C, int64_t F
   Ffn f{t, C, F, act, 1, x, wg, wu, wd, nullptr, st, wait_ns, nullptr, nullptr};
   TRY(operands(f, f32, w, (char*)ws, s));
   char* b = (char*)ws;
-  return f32 ? fwd<true>(f, y, b + w.a, s) : fwd<false>(f, y, b + w.a, s);
+  float* part = (float*)(b + w.part);
+  return f32 ? fwd<true>(f, y, b + w.a, part, s) : fwd<false>(f, y, b + w.a, part, s);
 }
 
 cudaError_t ffn_bwd_dispatch(int dtype, int act, int64_t t, int64_t C, int64_t F, const void* x,
@@ -860,8 +986,9 @@ cudaError_t ffn_bwd_dispatch(int dtype, int act, int64_t t, int64_t C, int64_t F
   char* b = (char*)ws;
   TRY(operands(f, f32, w, b, s));
   float *g = (float*)(b + w.g), *u = (float*)(b + w.u), *d32 = (float*)(b + w.d32);
-  return f32 ? bwd<true>(f, gx, gwg, gwu, gwd, b + w.a, b + w.d, d32, g, u, s)
-             : bwd<false>(f, gx, gwg, gwu, gwd, b + w.a, b + w.d, nullptr, g, u, s);
+  float* part = (float*)(b + w.part);
+  return f32 ? bwd<true>(f, gx, gwg, gwu, gwd, b + w.a, b + w.d, d32, g, u, part, s)
+             : bwd<false>(f, gx, gwg, gwu, gwd, b + w.a, b + w.d, nullptr, g, u, part, s);
 }
 
 #undef TRY

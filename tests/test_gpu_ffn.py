@@ -318,3 +318,18 @@ def test_largest_offsets(mhc):
     f = slice(F - 32, F)
     ref = R.ffn_grad(x, wg[f], wu[f], wd[:, f], gy, "silu")
     assert R.norm_rel(gwg[f], ref[1]) < 2.0 ** -7 and R.norm_rel(gwd[:, f], ref[3]) < 2.0 ** -7
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,C,F", [(8000, 64, 64), (4001, 136, 72), (300, 72, 8200),
+                                   (1030, 2056, 136), (7, 64, 6656), (258, 8, 16384)])
+def test_long_sums_with_few_results(mhc, T, C, F, dtype):
+    """Products whose sums are split over the machine: long in tokens, in hidden units or in
+    channels against a small result; twice, for the same bits."""
+    x, wg, wu, wd, gy = _case(T, C, F, dtype, 16)
+    y = mhc.mhc_ffn(x, wg, wu, wd)
+    _check_fwd(y, x, wg, wu, wd, "silu", dtype)
+    got = mhc.mhc_ffn_backward(x, wg, wu, wd, gy)
+    _check_bwd(got, x, wg, wu, wd, gy, "silu", dtype)
+    again = mhc.mhc_ffn(x, wg, wu, wd), *mhc.mhc_ffn_backward(x, wg, wu, wd, gy)
+    assert all(torch.equal(a, b) for a, b in zip((y, *got), again))
