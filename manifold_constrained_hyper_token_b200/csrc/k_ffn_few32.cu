@@ -16,8 +16,8 @@
 // accumulators, orders 1 and 2 together.
 //
 // The tensor cores' adder cuts instead of rounding, so a long sum is spread over up
-// to four sets of accumulators in turn, and a CTA's share of k is at most kMaxK per
-// set; the rest of the sum is rounded fp32 addition in the epilogue.
+// to four sets of accumulators in turn and over the cluster, kGoodK per set where
+// eight CTAs allow it; the rest of the sum is rounded fp32 addition in the epilogue.
 //
 // Warps: 0 weights' TMA, 1 the MMAs, 2 the tokens' TMA, 4-19 the split; then all of
 // them the reduction over the cluster, as in k_ffn_few.cu.  Every warp takes part in
@@ -39,7 +39,7 @@ constexpr int PLANE = TM * TK * 2;    // ... one of its planes
 constexpr int NT = 640, NCONV = 16;   // threads; splitting warps
 constexpr int MAXRAW = 6;
 constexpr int ROOM = 222 * 1024, TAIL = 1024 + 512;
-constexpr int kMaxK = 2048;
+constexpr int kMaxK = 2048, kGoodK = 1024;  // k per set of accumulators: at most; aimed at
 static_assert(RAW / 2 == 32 * NCONV * 16, "a thread takes 16 bytes of each half of a tile");
 }  // namespace few32
 
@@ -434,7 +434,7 @@ cudaError_t launch(Few32P& P, const FewArgs& f, int64_t K, cudaStream_t s) {
   int parts = 0;
   int64_t best = 0;
   for (int p = 1; p <= 8 && p <= nk; p *= 2) {
-    if ((int64_t)(nk + p - 1) / p * TK > (int64_t)kMaxK * P.sets && p < 8 && 2 * p <= nk)
+    if ((int64_t)(nk + p - 1) / p * TK > (int64_t)kGoodK * P.sets && p < 8 && 2 * p <= nk)
       continue;
     const int64_t cost = ((tiles * p + slots - 1) / slots) * ((nk + p - 1) / p + 6);
     if (parts == 0 || cost < best) {

@@ -53,7 +53,7 @@ constexpr int HALF = 128;         // rows of A that one CTA brings
 constexpr int NEPI = 4;           // epilogue warps
 constexpr int NT = 256;
 constexpr int BAND = 8;
-constexpr int kChunk = 16;        // fp32: k blocks per stay of the first planes' products
+constexpr int kChunk = 8;         // fp32: k blocks per stay of the first planes' products
 constexpr int BOX = 32 * 64;      // a staged box of results: 32 rows of 32 bf16 or 16 fp32
 
 template <int TN, bool F32> struct Cfg {
