@@ -39,7 +39,7 @@ constexpr int PLANE = TM * TK * 2;    // ... one of its planes
 constexpr int NT = 640, NCONV = 16;   // threads; splitting warps
 constexpr int MAXRAW = 6;
 constexpr int ROOM = 222 * 1024, TAIL = 1024 + 512;
-constexpr int kMaxK = 2048, kGoodK = 1024;  // k per set of accumulators: at most; aimed at
+constexpr int kMaxK = 2048, kGoodK = 512;  // k per set of accumulators: at most; aimed at
 static_assert(RAW / 2 == 32 * NCONV * 16, "a thread takes 16 bytes of each half of a tile");
 }  // namespace few32
 
