@@ -32,7 +32,8 @@
 // The backward's g and u are kept in fp32: rounded to bf16 they would put as much
 // error into dg and du as these take from their own rounding.
 //
-// Warps of a CTA: 0 TMA; 1 the MMAs (first CTA only); 2 TMEM; 4-7 the epilogue.
+// Warps of a CTA: 0 TMA; 1 the MMAs (first CTA only); 2 TMEM; from 4 on the
+// epilogue.
 // Both CTAs' copies complete on the first CTA's barriers.  (A thread of the
 // second CTA that waited for its copies and then arrived there, an arrive with
 // release at cluster scope, took about 0.9 us per stage: 600 TFLOP/s in all.)
@@ -50,13 +51,13 @@ namespace mhc {
 namespace ftc {
 constexpr int TM = 256;           // the pair's rows
 constexpr int HALF = 128;         // rows of A that one CTA brings
-constexpr int NEPI = 4;           // epilogue warps
-constexpr int NT = 256;
 constexpr int BAND = 8;
 constexpr int kChunk = 8;         // fp32: k blocks per stay of the first planes' products
 constexpr int BOX = 32 * 64;      // a staged box of results: 32 rows of 32 bf16 or 16 fp32
 
-template <int TN, bool F32> struct Cfg {
+template <int TN, bool F32, bool MORE> struct Cfg {
+  static constexpr int NEPI = MORE ? 8 : 4;             // epilogue warps
+  static constexpr int NT = 128 + 32 * NEPI;
   static constexpr int TK = F32 ? 32 : 64;              // k block
   static constexpr int NP = F32 ? 3 : 1;                // planes of an operand
   static constexpr int NS = F32 ? 4 : 6;                // stages
@@ -64,7 +65,7 @@ template <int TN, bool F32> struct Cfg {
   static constexpr int APLANE = HALF * TK * 2, BPLANE = BROWS * TK * 2;
   static constexpr int ABYTES = NP * APLANE;
   static constexpr int STAGE = ABYTES + NP * BPLANE;
-  static constexpr int OUT = F32 ? 16384 : 8192;        // staged results per epilogue warp
+  static constexpr int OUT = (F32 ? 65536 : 32768) / NEPI;  // staged results per such warp
   static constexpr int OUT_OFF = NS * STAGE;
   static constexpr int BAR_OFF = OUT_OFF + NEPI * OUT;
   static constexpr int SMEM = BAR_OFF + 256 + 1024;
@@ -78,6 +79,10 @@ template <int TN, bool F32> struct Cfg {
 namespace {
 
 enum Epi { EPI_STORE, EPI_GATE, EPI_KEEP, EPI_DGATE, EPI_PART };
+
+// DGATE has the longest epilogue: eight warps, two to a TMEM lane quarter (T = 2368,
+// C = 4096, F = 4736: 143 us with four warps, 121 with g and u fetched ahead as well).
+constexpr bool more_warps(Epi e, bool f32) { return e == EPI_DGATE && !f32; }
 
 // One launch: the sum of nseg products into each tile, the s-th of A's planes
 // from s NP on by B's map s.
@@ -198,10 +203,11 @@ __device__ __forceinline__ void row16(const float* base, int64_t row, int64_t co
 }
 
 template <Epi E, bool AMN, bool BMN, bool F32, int TN>
-__global__ void __launch_bounds__(ftc::NT, 1)
+__global__ void __launch_bounds__(ftc::Cfg<TN, F32, more_warps(E, F32)>::NT, 1)
     k_ffn_tc(const __grid_constant__ GemmArgs P) {
   using namespace ftc;
-  using G = Cfg<TN, F32>;
+  using G = Cfg<TN, F32, more_warps(E, F32)>;
+  constexpr int NEPI = G::NEPI;
   constexpr int STAGE = G::STAGE, NS = G::NS, TK = G::TK, HN = TN / 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -386,7 +392,10 @@ __global__ void __launch_bounds__(ftc::NT, 1)
     static_assert(SETS >= 1, "staged results");
     constexpr int COLS = DUAL ? HN : TN;  // columns of D's tile
     const int q = warp & 3;               // TMEM lane quarter this warp may read
-    uint8_t* out = smem + G::OUT_OFF + q * G::OUT;
+    uint8_t* out = smem + G::OUT_OFF + (warp - 4) * G::OUT;
+    // this warp's columns of the tile: all, or half
+    constexpr int MINE = COLS * 4 / NEPI;
+    const int first = (warp - 4) / 4 * MINE;
     const uint32_t sums = tmem + ((uint32_t)(32 * q) << 16) + G::SUMS;
     // a tile's products may rightly take longer than one wait: 4 us per k block more
     const uint64_t tile_ns = P.wait_ns + (uint64_t)P.nseg * P.kblocks * 4000;
@@ -396,6 +405,14 @@ __global__ void __launch_bounds__(ftc::NT, 1)
       tile_at(P, id, z, mi, ni, ja, jb);
       const int64_t row0 = (int64_t)mi * TM + rank * HALF + 32 * q, row = row0 + lane;
       bool ok = true;
+      // DGATE: g and u are fetched 16 columns ahead, the first ones under the products
+      // (without, their latency made the epilogue 43 us a tile, against 28 us of
+      // products at k = 4096)
+      float gnext[16], unext[16];
+      if (E == EPI_DGATE) {
+        row16(P.g, row, (int64_t)ni * COLS + first, P.M, P.N, gnext);
+        row16(P.u, row, (int64_t)ni * COLS + first, P.M, P.N, unext);
+      }
       for (int j0 = ja, j1; j0 < jb; j0 = j1, ++n) {
         j1 = stay_end<F32>(j0, jb);
         const int buf = n & 1;
@@ -434,7 +451,7 @@ __global__ void __launch_bounds__(ftc::NT, 1)
         if (j1 == jb) {
           const uint32_t at = F32 ? sums : ta;  // D's columns
 #pragma unroll 1
-          for (int c = 0; c < COLS; c += WIDE ? 64 : 32) {
+          for (int c = first; c < first + MINE; c += WIDE ? 64 : 32) {
             const int64_t col = (int64_t)ni * COLS + c;
             const bool in = row0 < P.M && col < P.N;
             uint8_t* box = out + (nset++ % SETS) * SET;
@@ -485,8 +502,15 @@ __global__ void __launch_bounds__(ftc::NT, 1)
                 }
               } else {
                 float u[16], gv[16];
-                row16(P.g, row, col + 16 * g, P.M, P.N, gv);
-                row16(P.u, row, col + 16 * g, P.M, P.N, u);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  gv[i] = gnext[i];
+                  u[i] = unext[i];
+                }
+                if (cg + 16 < first + MINE) {
+                  row16(P.g, row, col + 16 * g + 16, P.M, P.N, gnext);
+                  row16(P.u, row, col + 16 * g + 16, P.M, P.N, unext);
+                }
                 tc::tmem_get16(at + cg, v);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -659,7 +683,7 @@ struct Opnds {
 template <Epi E, bool AMN, bool BMN, bool F32, int TN>
 cudaError_t launch_tn(GemmArgs& P, const Opnds& o, cudaStream_t s) {
   constexpr bool DUAL = E == EPI_GATE || E == EPI_KEEP;
-  using G = ftc::Cfg<TN, F32>;
+  using G = ftc::Cfg<TN, F32, more_warps(E, F32)>;
   TRY(operand_map(&P.a, o.a, AMN, ftc::HALF, G::NP));
   TRY(operand_map(&P.b[0], o.b[0], BMN, G::BROWS, G::NP));
   if (o.b[1].p) TRY(operand_map(&P.b[1], o.b[1], BMN, G::BROWS, G::NP));
@@ -669,7 +693,7 @@ cudaError_t launch_tn(GemmArgs& P, const Opnds& o, cudaStream_t s) {
   auto kern = k_ffn_tc<E, AMN, BMN, F32, TN>;
   TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM));
   const int64_t tiles = (int64_t)P.mt * P.nt * P.nz * P.split, pairs = sm_pairs();
-  return launch_after(kern, (unsigned)(2 * (tiles < pairs ? tiles : pairs)), ftc::NT, G::SMEM, 2, s,
+  return launch_after(kern, (unsigned)(2 * (tiles < pairs ? tiles : pairs)), G::NT, G::SMEM, 2, s,
                       P);
 }
 
