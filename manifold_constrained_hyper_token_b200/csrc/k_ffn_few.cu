@@ -45,6 +45,7 @@ struct FewP {
   float *g, *u;          // GATE: kept unless null; DGATE: read
   int act;
   bool early;            // a later kernel of its call: the weights may be read at once
+  bool beside;           // needs nothing from the kernel before it
   uint32_t tmem_cols, acc1;  // columns to allocate; the second accumulator's column
   int* status;
   uint64_t wait_ns;
@@ -128,7 +129,7 @@ __global__ void __launch_bounds__(few::NT) k_ffn_few(const __grid_constant__ Few
   const int ahead = !P.early ? 0 : blocks < P.stages ? blocks : P.stages;
   if (loader)
     for (int it = 0; it < ahead; ++it) load_weights(it);
-  tc::grid_wait();
+  if (!P.beside) tc::grid_wait();
   tc::grid_release();
 
   if (loader) {
@@ -272,6 +273,7 @@ __global__ void __launch_bounds__(few::NT) k_ffn_few(const __grid_constant__ Few
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, P.tmem_cols);
   }
+  if (P.beside) tc::grid_wait();
 }
 
 #define TRY(call)                         \
@@ -373,7 +375,7 @@ cudaError_t few_down(const FewArgs& f, const void* a, void* y, cudaStream_t s) {
 
 cudaError_t few_dgate(const FewArgs& f, const float* g, const float* u, void* d, cudaStream_t s) {
   FewP P = base(f, f.F, 1);
-  P.early = true;
+  P.beside = true;
   TRY(weight_map(&P.w[0], f.wd, f.C, f.F, true));
   TRY(token_map(&P.x, f.gy, f.t, f.C, 1, P.np));
   P.o0 = (bf16*)d;

@@ -55,6 +55,7 @@ struct Few32P {
   float *g, *u;            // GATE: kept unless null; DGATE: read
   int act;
   bool early;              // a later kernel of its call: the weights may be read at once
+  bool beside;             // needs nothing from the kernel before it
   uint32_t tmem_cols;      // columns to allocate; an accumulator has np
   int* status;
   uint64_t wait_ns;
@@ -129,7 +130,9 @@ __global__ void __launch_bounds__(few32::NT, 1) k_ffn_few32(const __grid_constan
   };
 
   // the weights' loader needs nothing from the kernel before this one
-  if (warp != 0 || !P.early) {
+  if (P.beside) {
+    tc::grid_release();
+  } else if (warp != 0 || !P.early) {
     tc::grid_wait();
     tc::grid_release();
   }
@@ -370,6 +373,7 @@ __global__ void __launch_bounds__(few32::NT, 1) k_ffn_few32(const __grid_constan
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, P.tmem_cols);
   }
+  if (P.beside) tc::grid_wait();
 }
 
 #define TRY(call)                         \
@@ -486,7 +490,7 @@ cudaError_t few32_down(const FewArgs& f, const void* a, float* y, cudaStream_t s
 
 cudaError_t few32_dgate(const FewArgs& f, const float* g, const float* u, void* d, cudaStream_t s) {
   Few32P P = base(f, f.F, 1);
-  P.early = true;
+  P.beside = true;
   TRY(weight_map(&P.w[0], f.wd, f.C, f.F, true));
   TRY(token_map(&P.x, f.gy, f.t, f.C, 3, P.np));
   P.o0 = d;

@@ -35,6 +35,7 @@ struct OneP {
   float *g, *u;                // GATE: kept unless null; DGATE: read
   int act;
   bool early;                  // a later kernel of its call: weights may be read at once
+  bool beside;                 // COLS: needs nothing from the kernel before it
 };
 
 __device__ __forceinline__ float4 ld_once(const float* p) {
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(NTHR) k_cols(const __grid_constant__ OneP P) {
   float acc[TT][4] = {};
   float4 next[8];
   if (P.early && c0 < c1) fetch(c0, next);
-  tc::grid_wait();
+  if (!P.beside) tc::grid_wait();
   tc::grid_release();
   if (c0 < c1) {
     if (!P.early) fetch(c0, next);
@@ -286,6 +287,7 @@ __global__ void __launch_bounds__(NTHR) k_cols(const __grid_constant__ OneP P) {
   __syncwarp();
   // nobody reads this CTA's part any more
   if (P.parts > 1) tc::cluster_sync();
+  if (P.beside) tc::grid_wait();
 }
 
 int sm_count() {
@@ -344,13 +346,13 @@ template <OneEpi E> cudaError_t cols(OneP& P, cudaStream_t s) {
 cudaError_t one32_gate(const FewArgs& f, float* a, void* planes, float* g, float* u,
                        cudaStream_t s) {
   OneP P{{(const float*)f.wg, (const float*)f.wu}, (const float*)f.x, f.C, f.F, f.t, 1, 1, a,
-         (__nv_bfloat16*)planes, g, u, f.act, false};
+         (__nv_bfloat16*)planes, g, u, f.act, false, false};
   return rows<ONE_GATE>(P, s);
 }
 
 cudaError_t one32_down(const FewArgs& f, const float* a, float* y, cudaStream_t s) {
   OneP P{{(const float*)f.wd, nullptr}, a, f.F, f.C, f.t, 1, 1, y, nullptr, nullptr, nullptr, 0,
-         true};
+         true, false};
   return rows<ONE_STORE>(P, s);
 }
 
@@ -358,13 +360,13 @@ cudaError_t one32_dgate(const FewArgs& f, const float* g, const float* u, float*
                         cudaStream_t s) {
   OneP P{{(const float*)f.wd, nullptr}, (const float*)f.gy, f.C, f.F, f.t, 1, 1, d,
          (__nv_bfloat16*)planes, const_cast<float*>(g), const_cast<float*>(u), f.act,
-         true};
+         true, true};
   return cols<ONE_DGATE>(P, s);
 }
 
 cudaError_t one32_grad_x(const FewArgs& f, const float* d, float* gx, cudaStream_t s) {
   OneP P{{(const float*)f.wg, (const float*)f.wu}, d, f.F, f.C, f.t, 2, 1, gx, nullptr, nullptr,
-         nullptr, 0, true};
+         nullptr, 0, true, false};
   return cols<ONE_STORE>(P, s);
 }
 

@@ -862,29 +862,40 @@ cudaError_t bwd(const Ffn& f, void* gx, void* gwg, void* gwu, void* gwd, void* a
   const Mat WG{f.wg, f.F, f.C, np, false}, WU{f.wu, f.F, f.C, np, false};
   const Mat WD{f.wd, f.C, f.F, np, false};
   const bool few = f.is_few();
+  const Parts parts = parts_of(F32, few, f.t, f.C, f.F);
+  JoinArgs J{};
+  int joins = 0;
+  // Five products: g and u with a; gw_down, which needs a; dg and du, which need g
+  // and u and run beside it; gx, which needs dg and du; gw_gate and gw_up beside it.
+  // Those beside another fill the SMs that it leaves idle.
   if (f.is_one()) {
     TRY(one32_gate(f.one(), nullptr, a, g, u, s));
-    TRY(one32_dgate(f.one(), g, u, d32, d, s));
   } else if (few && F32) {
     TRY(few32_gate(f.few(), a, g, u, s));
-    TRY(few32_dgate(f.few(), g, u, d, s));
   } else if (few) {
     TRY(few_gate(f.few(), a, g, u, s));
-    TRY(few_dgate(f.few(), g, u, d, s));
   } else {
     TRY(gate_product<F32>(f, a, g, u, s));
+  }
+  {
+    GemmArgs P = base_args(f, 1, f.C, f.F);
+    TRY((plain_product<true, true, F32>(P, {GY, {A}, f.t}, &gwd, part + parts.gwd, J, joins, s)));
+  }
+  if (f.is_one()) {
+    TRY(one32_dgate(f.one(), g, u, d32, d, s));
+  } else if (few && F32) {
+    TRY(few32_dgate(f.few(), g, u, d, s));
+  } else if (few) {
+    TRY(few_dgate(f.few(), g, u, d, s));
+  } else {
     GemmArgs P = base_args(f, 1, f.t, f.F);
     TRY(result_map(&P.d[0], D, false));
     P.g = g;
     P.u = u;
+    P.beside = true;
     TRY((launch<EPI_DGATE, false, true, F32>(
         P, {GY, {WD}, f.C}, plan(F32, false, false, f.t, f.F, 1, f.C, 1).tn, s)));
   }
-  const Parts parts = parts_of(F32, few, f.t, f.C, f.F);
-  JoinArgs J{};
-  int joins = 0;
-  // the rest needs only what is finished when the next kernel starts: the three
-  // run beside one another, each filling the SMs that the one before leaves idle
   if (f.is_one()) {
     TRY(one32_grad_x(f.one(), d32, (float*)gx, s));
   } else if (few && F32) {
@@ -896,17 +907,12 @@ cudaError_t bwd(const Ffn& f, void* gx, void* gwg, void* gwu, void* gwd, void* a
     TRY((plain_product<false, true, F32>(P, {D, {WG, WU}, f.F}, &gx, part + parts.gx, J, joins,
                                          s)));
   }
-  {
-    GemmArgs P = base_args(f, 1, f.F, f.C);
-    P.nz = 2;
-    P.zplanes = np;
-    P.beside = true;
-    void* const out[2] = {gwg, gwu};
-    TRY((plain_product<true, true, F32>(P, {D, {X}, f.t}, out, part + parts.gw, J, joins, s)));
-  }
-  GemmArgs P = base_args(f, 1, f.C, f.F);
+  GemmArgs P = base_args(f, 1, f.F, f.C);
+  P.nz = 2;
+  P.zplanes = np;
   P.beside = true;
-  TRY((plain_product<true, true, F32>(P, {GY, {A}, f.t}, &gwd, part + parts.gwd, J, joins, s)));
+  void* const out[2] = {gwg, gwu};
+  TRY((plain_product<true, true, F32>(P, {D, {X}, f.t}, out, part + parts.gw, J, joins, s)));
   return join<F32>(J, joins, s);
 }
 
