@@ -262,6 +262,7 @@ __global__ void __launch_bounds__(ftc::Cfg<TN, F32, more_warps(E, F32)>::NT, 1)
 
   auto give_up = [&]() {
     *abort_flag = 1;
+    tc::st_cluster_u32(tc::map_cta(tc::smem_u32(tmem_slot + 1), (uint32_t)(rank ^ 1)), 1u);
     flag_status(P.status, MHC_ERR_TIMEOUT);
   };
 
@@ -296,20 +297,6 @@ __global__ void __launch_bounds__(ftc::Cfg<TN, F32, more_warps(E, F32)>::NT, 1)
             kb = 0;
             ++seg;
           }
-        }
-      }
-      // Every copy has landed before the CTA can exit.  After an ordinary run the
-      // MMAs have waited for all of them; after a give-up the first CTA waits for
-      // the rounds that both CTAs issued, and the second, whose copies may be
-      // ahead of the first CTA's count, for a millisecond.
-      if (rank == 0) {
-        for (int64_t i = it > NS ? it - NS : 0; i < it; ++i)
-          if (!tc::mbar_wait(full((int)(i % NS)), (uint32_t)(i / NS) & 1u, nullptr,
-                             tc::kDrainWaitNs))
-            break;
-      } else if (!ok) {
-        const uint64_t t0 = tc::global_ns();
-        while (tc::global_ns() - t0 < 1000000) {
         }
       }
     }
@@ -560,6 +547,17 @@ __global__ void __launch_bounds__(ftc::Cfg<TN, F32, more_warps(E, F32)>::NT, 1)
   tc::tc_fence_before();
   __syncthreads();
   tc::cluster_sync();  // no arrival or MMA of the partner is under way any more
+  // After an ordinary run the MMAs have waited for every copy.  When either CTA gave
+  // up, copies may be on their way that no barrier of the first CTA counts any more
+  // (the two need not have issued the same ones): a millisecond, a thousand times
+  // what a copy takes, and both are done.
+  if (*abort_flag) {  // of both CTAs, or of neither
+    const uint64_t t0 = tc::global_ns();
+    while (tc::global_ns() - t0 < 1000000) {
+    }
+    __syncwarp();
+    tc::cluster_sync();
+  }
   // the last commit of the first CTA has arrived here too
   if (rank == 1 && threadIdx.x == 0) tc::mbar_wait(fin_bar, 0, nullptr, tc::kDrainWaitNs);
   if (warp == 2) {

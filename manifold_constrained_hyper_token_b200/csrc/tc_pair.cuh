@@ -191,6 +191,10 @@ __device__ __forceinline__ void tmem_put16(uint32_t taddr, const float (&v)[16])
       : "memory");
 }
 
+// A word into the cluster's shared memory (an address from map_cta).
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 // Four floats of the cluster's shared memory (an address from map_cta).
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
   float4 v;
@@ -221,7 +225,9 @@ cudaError_t launch_after(void (*kern)(P...), unsigned grid, unsigned block, size
   c.stream = s;
   c.attrs = at;
   c.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&c, kern, args...);
+  const cudaError_t e = cudaLaunchKernelEx(&c, kern, args...);
+  if (e != cudaSuccess) cudaGetLastError();  // reported here, not by a later check
+  return e;
 }
 
 }  // namespace mhc
