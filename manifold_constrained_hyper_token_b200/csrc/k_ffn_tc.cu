@@ -80,9 +80,13 @@ namespace {
 
 enum Epi { EPI_STORE, EPI_GATE, EPI_KEEP, EPI_DGATE, EPI_PART };
 
-// DGATE has the longest epilogue: eight warps, two to a TMEM lane quarter (T = 2368,
-// C = 4096, F = 4736: 143 us with four warps, 121 with g and u fetched ahead as well).
-constexpr bool more_warps(Epi e, bool f32) { return e == EPI_DGATE && !f32; }
+// The epilogues with arithmetic take eight warps, two to a TMEM lane quarter: DGATE,
+// T = 2368, C = 4096, F = 4736, 143 us with four warps, 116 with eight and g and u
+// fetched ahead; T = 4096, C = F = 1024, forward pass (GATE) 47 -> 39 us, backward
+// (KEEP) 134 -> 125.  Plain results gained nothing; fp32 stages more and has no room.
+constexpr bool more_warps(Epi e, bool f32) {
+  return !f32 && (e == EPI_GATE || e == EPI_KEEP || e == EPI_DGATE);
+}
 
 // One launch: the sum of nseg products into each tile, the s-th of A's planes
 // from s NP on by B's map s.
@@ -373,10 +377,12 @@ __global__ void __launch_bounds__(ftc::Cfg<TN, F32, more_warps(E, F32)>::NT, 1)
     constexpr bool PLAIN = E == EPI_STORE || E == EPI_PART;
     constexpr int SET = PLAIN           ? 2 * BOX
                         : E == EPI_GATE ? NB * BOX
-                        : E == EPI_KEEP ? (2 + NB) * BOX
+                        : E == EPI_KEEP ? (F32 ? 2 + NB : 2) * BOX
                                         : 2 * NB * BOX;
     constexpr int SETS = G::OUT / SET > 4 ? 4 : G::OUT / SET;
     static_assert(SETS >= 1, "staged results");
+    // KEEP's a has boxes of its own in fp32, in bf16 it follows g and u through theirs
+    constexpr int AOFF = E == EPI_KEEP && F32 ? 2 * BOX : 0;
     constexpr int COLS = DUAL ? HN : TN;  // columns of D's tile
     const int q = warp & 3;               // TMEM lane quarter this warp may read
     uint8_t* out = smem + G::OUT_OFF + (warp - 4) * G::OUT;
@@ -444,6 +450,7 @@ __global__ void __launch_bounds__(ftc::Cfg<TN, F32, more_warps(E, F32)>::NT, 1)
             uint8_t* box = out + (nset++ % SETS) * SET;
             const uint32_t bu = tc::smem_u32(box);
             const int cc = (int)col, rr = (int)row0;
+            float hold[16];
             if (lane == 0) tc::bulk_wait_read<SETS - 1>();
             __syncwarp();
 #pragma unroll 1
@@ -472,11 +479,6 @@ __global__ void __launch_bounds__(ftc::Cfg<TN, F32, more_warps(E, F32)>::NT, 1)
                   }
                   put_f32(box, lane, v);
                   put_f32(box + BOX, lane, u);
-                }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = gate<!F32>(P.act, v[i]) * u[i];
-                put_operand<F32>(box + (E == EPI_KEEP ? 2 * BOX : 0), lane, g, v);
-                if (E == EPI_KEEP) {
                   tc::fence_proxy_async_smem();
                   __syncwarp();
                   if (lane == 0) {
@@ -484,8 +486,23 @@ __global__ void __launch_bounds__(ftc::Cfg<TN, F32, more_warps(E, F32)>::NT, 1)
                       tc::tma_store_3d(&P.d[1], bu, cc + 16 * g, rr, 0);
                       tc::tma_store_3d(&P.d[2], bu + BOX, cc + 16 * g, rr, 0);
                     }
-                    if (g == 0) tc::bulk_commit();
+                    tc::bulk_commit();
                   }
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = gate<!F32>(P.act, v[i]) * u[i];
+                if (E == EPI_GATE) {
+                  put_operand<F32>(box, lane, g, v);
+                } else if (g == 0) {
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) hold[i] = v[i];
+                } else {
+                  if (!F32) {
+                    if (lane == 0) tc::bulk_wait_read<0>();
+                    __syncwarp();
+                  }
+                  put_operand<F32>(box + AOFF, lane, 0, hold);
+                  put_operand<F32>(box + AOFF, lane, 1, v);
                 }
               } else {
                 float u[16], gv[16];
@@ -526,8 +543,7 @@ __global__ void __launch_bounds__(ftc::Cfg<TN, F32, more_warps(E, F32)>::NT, 1)
                     tc::tma_store_3d(&P.d[0], bu + pl * BOX, cc, rr, pl);
                 } else {
                   for (int pl = 0; pl < NB; ++pl)
-                    tc::tma_store_3d(&P.d[0], bu + (E == EPI_KEEP ? 2 * BOX : 0) + pl * BOX, cc,
-                                     rr, pl);
+                    tc::tma_store_3d(&P.d[0], bu + AOFF + pl * BOX, cc, rr, pl);
                 }
               }
               tc::bulk_commit();
