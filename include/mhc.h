@@ -414,8 +414,9 @@ typedef struct mhc_norm_params {
  *   in : x [T][C] (dtype), weight [C] float32, bias [C] float32 or NULL (no bias)
  *   out: y [T][C] (dtype)
  * dev_status gets MHC_ERR_NONFINITE when a token's mean or 1/sqrt(var + eps)
- * is not finite (a non-finite input, or a constant row with eps = 0); only
- * that token's row of y is then undefined.  No workspace.
+ * is not finite (a non-finite input, or a constant row with eps = 0) or the sum
+ * of (x[c] - mean)^2 is above float32's largest value; only that token's row of y
+ * is then undefined.  No workspace.
  */
 MHC_API mhc_status mhc_layer_norm(const mhc_norm_params *p, const void *x, const float *weight,
                                   const float *bias, void *y, int *dev_status,

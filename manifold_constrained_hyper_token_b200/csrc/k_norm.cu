@@ -89,8 +89,9 @@ struct Share {
   float m, m2, a, ax;
 };
 
+// s is 0 only where the variance left fp32's range.
 __device__ __forceinline__ void report(float mean, float s, int* status) {
-  if (!isfinite(mean) || !isfinite(s)) flag_status(status, MHC_ERR_NONFINITE);
+  if (!isfinite(mean) || !isfinite(s) || s == 0.f) flag_status(status, MHC_ERR_NONFINITE);
 }
 
 // Channels that warp `warp` of a row of nvec vectors holds: vectors 32 warp + lane,

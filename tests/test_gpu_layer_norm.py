@@ -104,6 +104,24 @@ def test_nonfinite_rows_stay_alone(mhc, C, dtype, bad):
                     R.norm_grad_bound(x[keep], w, gy[keep], 1e-6, dtype)[0], "grad_x")
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,C", [(5, 64), (5, 1032), (2500, 1024), (2500, 1032), (5, 40000)])
+def test_squares_beyond_fp32_are_reported(mhc, T, C, dtype):
+    """Deviations of 2^70 have squares that fp32 cannot hold; 2^40 fits."""
+    x, w, b, gy = _case(T, C, dtype, C)
+    xd, wd, bd, gd = x.cuda(), w.cuda(), b.cuda(), gy.cuda()
+    for scale, want in ((2.0 ** 40, 0), (2.0 ** 70, NONFINITE)):
+        big = xd.clone()
+        big[T - 2] *= scale
+        st = torch.zeros(2, dtype=torch.int32, device="cuda")
+        y = mhc.mhc_layer_norm(big, wd, bd, dev_status=st[:1]).cpu()
+        mhc.mhc_layer_norm_backward(big, wd, gd, dev_status=st[1:])
+        assert st.tolist() == [want, want]
+        keep = [t for t in range(T) if want == 0 or t != T - 2]
+        xs = big.cpu()[keep]
+        R.assert_within(y[keep], R.norm(xs, w, b, 1e-6), R.norm_bound(xs, w, b, 1e-6, dtype), "y")
+
+
 @pytest.mark.parametrize("T,C", [(1000, 64), (777, 7168), (70, 40000)])
 def test_repeats_bit_for_bit_and_writes_nothing_else(mhc, T, C):
     x, w, b, gy = _case(T, C, BF16, 3)
