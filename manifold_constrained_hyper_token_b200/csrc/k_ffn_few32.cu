@@ -37,7 +37,7 @@ constexpr int TM = 128, TK = 32;
 constexpr int RAW = TM * TK * 4;      // a weight tile in fp32
 constexpr int PLANE = TM * TK * 2;    // ... one of its planes
 constexpr int NT = 640, NCONV = 16;   // threads; splitting warps
-constexpr int MAXRAW = 6;
+constexpr int MAXRAW = 12, MAXX = 6;  // ring stages, at most: weight tiles, k blocks of tokens
 constexpr int ROOM = 222 * 1024, TAIL = 1024 + 512;
 constexpr int kMaxK = 2048, kGoodK = 512;  // k per set of accumulators: at most; aimed at
 static_assert(RAW / 2 == 32 * NCONV * 16, "a thread takes 16 bytes of each half of a tile");
@@ -48,7 +48,7 @@ enum Epi32 { F32_STORE, F32_GATE, F32_DGATE };
 struct Few32P {
   CUtensorMap w[2], x;
   int nseg, kblocks;
-  int np, raws;            // tokens rounded up to 16; raw stages
+  int np, raws, xs;        // tokens rounded up to 16; weight tiles and token blocks on their way
   int sets, orders;        // accumulator sets of a weight; accumulators in a set (3, or 2)
   int64_t rows, t;
   void* o0;                // STORE: fp32 [t][rows]; else bf16 planes [3 or 6][t][rows]
@@ -77,20 +77,23 @@ __global__ void __launch_bounds__(few32::NT, 1) k_ffn_few32(const __grid_constan
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~(uintptr_t)1023);
-  // raw stages, then two sets of [weight][plane] tiles and the tokens' planes
-  const int xbytes = 3 * P.np * TK * 2, set_bytes = NW * 3 * PLANE + xbytes;
-  uint8_t* sets = smem + P.raws * NW * RAW;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sets + 2 * set_bytes);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * MAXRAW + 7);
+  // a ring of weight tiles, two sets of [weight][plane] tiles, a ring of tokens' planes
+  constexpr int SETB = NW * 3 * PLANE;
+  const int xbytes = 3 * P.np * TK * 2;
+  uint8_t* sets = smem + P.raws * RAW;
+  uint8_t* xring = sets + 2 * SETB;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(xring + P.xs * xbytes);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * MAXRAW + 2 * MAXX + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   auto raw_full = [&](int s) { return tc::smem_u32(bars + s); };
   auto raw_empty = [&](int s) { return tc::smem_u32(bars + MAXRAW + s); };
   auto set_full = [&](int s) { return tc::smem_u32(bars + 2 * MAXRAW + s); };
   auto set_empty = [&](int s) { return tc::smem_u32(bars + 2 * MAXRAW + 2 + s); };
   auto x_full = [&](int s) { return tc::smem_u32(bars + 2 * MAXRAW + 4 + s); };
-  const uint32_t done_bar = tc::smem_u32(bars + 2 * MAXRAW + 6);
+  auto x_empty = [&](int s) { return tc::smem_u32(bars + 2 * MAXRAW + 4 + MAXX + s); };
+  const uint32_t done_bar = tc::smem_u32(bars + 2 * MAXRAW + 4 + 2 * MAXX);
 
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   uint32_t csize;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
   const int parts = (int)csize, rank = (int)tc::cluster_rank();
@@ -108,7 +111,10 @@ __global__ void __launch_bounds__(few32::NT, 1) k_ffn_few32(const __grid_constan
     for (int s = 0; s < 2; ++s) {
       tc::mbar_init(set_full(s), NCONV);
       tc::mbar_init(set_empty(s), 1);
+    }
+    for (int s = 0; s < P.xs; ++s) {
       tc::mbar_init(x_full(s), 1);
+      tc::mbar_init(x_empty(s), 1);
     }
     tc::mbar_init(done_bar, 1);
     *abort_flag = 0;
@@ -141,8 +147,8 @@ __global__ void __launch_bounds__(few32::NT, 1) k_ffn_few32(const __grid_constan
     // ------------------------------------------------------- weights, as they are
     if (lane == 0) {
       const uint64_t stream = tc::policy_evict_first();
-      int it = 0;
-      for (; it < blocks; ++it) {
+      int it = 0;  // tiles: a k block has NW
+      for (; it < blocks * NW; ++it) {
         const int s = it % P.raws;
         if (it >= P.raws &&
             !tc::mbar_pipe_wait<false>(raw_empty(s), ((uint32_t)(it / P.raws) & 1u) ^ 1u,
@@ -150,19 +156,16 @@ __global__ void __launch_bounds__(few32::NT, 1) k_ffn_few32(const __grid_constan
           give_up();
           break;
         }
-        const int j = j0 + it, seg = j / P.kblocks, k0 = (j - seg * P.kblocks) * TK;
-        tc::mbar_arrive_expect_tx(raw_full(s), NW * RAW);
+        const int j = j0 + it / NW, seg = j / P.kblocks, k0 = (j - seg * P.kblocks) * TK;
+        tc::mbar_arrive_expect_tx(raw_full(s), RAW);
+        const CUtensorMap* m = &P.w[NW == 2 ? it % NW : seg];
+        const uint32_t dst = tc::smem_u32(smem + s * RAW);
+        if (MN) {
 #pragma unroll
-        for (int i = 0; i < NW; ++i) {
-          const CUtensorMap* m = &P.w[NW == 2 ? i : seg];
-          const uint32_t dst = tc::smem_u32(smem + (s * NW + i) * RAW);
-          if (MN) {
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-              tc::tma_load_2d(dst + b * (RAW / 4), m, raw_full(s), (int)row0 + 32 * b, k0, stream);
-          } else {
-            tc::tma_load_2d(dst, m, raw_full(s), k0, (int)row0, stream);
-          }
+          for (int b = 0; b < 4; ++b)
+            tc::tma_load_2d(dst + b * (RAW / 4), m, raw_full(s), (int)row0 + 32 * b, k0, stream);
+        } else {
+          tc::tma_load_2d(dst, m, raw_full(s), k0, (int)row0, stream);
         }
       }
       for (int i = it > P.raws ? it - P.raws : 0; i < it; ++i)
@@ -177,67 +180,89 @@ __global__ void __launch_bounds__(few32::NT, 1) k_ffn_few32(const __grid_constan
       const uint64_t keep = tc::policy_evict_last();
       int it = 0;
       for (; it < blocks; ++it) {
-        const int s = it & 1;
-        if (it >= 2 && !tc::mbar_pipe_wait<false>(set_empty(s), ((uint32_t)(it / 2) & 1u) ^ 1u,
-                                                  abort_flag, P.wait_ns)) {
+        const int s = it % P.xs;
+        if (it >= P.xs && !tc::mbar_pipe_wait<false>(x_empty(s), ((uint32_t)(it / P.xs) & 1u) ^ 1u,
+                                                     abort_flag, P.wait_ns)) {
           give_up();
           break;
         }
         const int j = j0 + it, seg = j / P.kblocks, k0 = (j - seg * P.kblocks) * TK;
         tc::mbar_arrive_expect_tx(x_full(s), xbytes);
-        tc::tma_load_3d(tc::smem_u32(sets + s * set_bytes + NW * 3 * PLANE), &P.x, x_full(s), k0,
-                        0, NW == 2 ? 0 : 3 * seg, keep);
+        tc::tma_load_3d(tc::smem_u32(xring + s * xbytes), &P.x, x_full(s), k0, 0,
+                        NW == 2 ? 0 : 3 * seg, keep);
       }
-      for (int i = it > 2 ? it - 2 : 0; i < it; ++i)
-        tc::mbar_wait(x_full(i & 1), (uint32_t)(i / 2) & 1u, nullptr, tc::kDrainWaitNs);
+      for (int i = it > P.xs ? it - P.xs : 0; i < it; ++i)
+        tc::mbar_wait(x_full(i % P.xs), (uint32_t)(i / P.xs) & 1u, nullptr, tc::kDrainWaitNs);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------------- MMA
-    if (lane == 0) {
-      for (int it = 0; it < blocks; ++it) {
-        const int s = it & 1;
-        const uint32_t par = (uint32_t)(it / 2) & 1u;
-        if (!tc::mbar_pipe_wait<false>(set_full(s), par, abort_flag, P.wait_ns) ||
-            !tc::mbar_pipe_wait<false>(x_full(s), par, abort_flag, P.wait_ns)) {
-          give_up();
-          break;
-        }
-        tc::tc_fence_after();
-        const uint32_t base = tc::smem_u32(sets + s * set_bytes);
+    // A small MMA is over before its operands are made up.  So the descriptors are
+    // prepared here (they count in 16 bytes), and the warp stays together and elects
+    // the lane that issues, which makes them uniform (T = 17, C = 7168, F = 14336:
+    // 633 us as a single lane's loop, 562 with the descriptors prepared, 441 so)
+    const bool leader = tc::elect_one();
+    const uint32_t np = (uint32_t)P.np, weight = (uint32_t)(P.sets * P.orders) * np;
+    const uint32_t id1 = tc::idesc_bf16(TM, P.np, MN, false);
+    const uint32_t idn = (np >> 3) << 17;  // one more np in N
+    const uint64_t adesc = MN ? tc::smem_desc(tc::smem_u32(sets), PLANE / 2, 1024, tc::SWZ_128B)
+                              : tc::smem_desc(tc::smem_u32(sets), 16, 512, tc::SWZ_64B);
+    const uint64_t bdesc = tc::smem_desc(tc::smem_u32(xring), 16, 512, tc::SWZ_64B);
+    int xs = 0, set = 0;
+    uint32_t xpar = 0, acc = tmem, add = 0;
+    for (int it = 0; it < blocks; ++it) {
+      const int s = it & 1;
+      const bool ok =
+          tc::mbar_pipe_wait<false>(x_full(xs), xpar, abort_flag, P.wait_ns) &&
+          tc::mbar_pipe_wait<false>(set_full(s), (uint32_t)(it / 2) & 1u, abort_flag, P.wait_ns);
+      if (!__all_sync(0xffffffffu, ok)) {
+        if (lane == 0) give_up();
+        break;
+      }
+      tc::tc_fence_after();
+      const uint64_t a0 = adesc + (uint32_t)(s * (SETB / 16));
+      const uint64_t b0 = bdesc + (uint32_t)(xs * (xbytes / 16));
 #pragma unroll
-        for (int k = 0; k < TK / 16; ++k) {
-          const int step = it * (TK / 16) + k, set = step % P.sets;
-          const bool add = step >= P.sets;
+      for (int k = 0; k < TK / 16; ++k) {
+        if (leader) {
 #pragma unroll
           for (int pw = 0; pw < 3; ++pw) {
 #pragma unroll
             for (int i = 0; i < NW; ++i) {
-              const uint32_t acc = tmem + (i * P.sets + set) * P.orders * P.np;
-              const uint32_t wb = base + (i * 3 + pw) * PLANE;
-              const uint64_t a = MN ? tc::smem_desc(wb + k * 2048, PLANE / 2, 1024, tc::SWZ_128B)
-                                    : tc::smem_desc(wb + k * 32, 16, 512, tc::SWZ_64B);
-              const uint32_t xb = base + NW * 3 * PLANE + k * 32;
+              const uint64_t a = a0 + (uint32_t)((i * 3 + pw) * (PLANE / 16) + k * (MN ? 128 : 2));
+              const uint64_t b = b0 + (uint32_t)(k * 2);
+              const uint32_t d = acc + i * weight;
               if (P.orders == 3) {
                 // X1 .. X(3 - pw), into the orders from pw on
-                tc::mma_bf16(acc + pw * P.np, a, tc::smem_desc(xb, 16, 512, tc::SWZ_64B),
-                             tc::idesc_bf16(TM, (3 - pw) * P.np, MN, false),
-                             add || pw > 0 ? 1u : 0u);
+                tc::mma_bf16(d + pw * np, a, b, id1 + (2 - pw) * idn, pw > 0 ? 1u : add);
               } else {
+#pragma unroll
                 for (int px = 0; px < 3 - pw; ++px)
-                  tc::mma_bf16(acc + (pw + px > 0 ? P.np : 0), a,
-                               tc::smem_desc(xb + px * P.np * 64, 16, 512, tc::SWZ_64B),
-                               tc::idesc_bf16(TM, P.np, MN, false),
-                               add || pw > 0 || px > 1 ? 1u : 0u);
+                  tc::mma_bf16(d + (pw + px > 0 ? np : 0), a, b + (uint32_t)px * np * 4, id1,
+                               pw > 0 || px > 1 ? 1u : add);
               }
             }
           }
         }
-        tc::mma_commit(set_empty(s));
+        acc += (uint32_t)P.orders * np;
+        if (++set == P.sets) {
+          set = 0;
+          acc = tmem;
+          add = 1;
+        }
       }
-      // the sums are complete, and no MMA is under way when TMEM is freed
-      tc::mma_commit(done_bar);
-      tc::mbar_wait(done_bar, 0, nullptr, tc::kDrainWaitNs);
+      if (leader) {
+        tc::mma_commit(set_empty(s));
+        tc::mma_commit(x_empty(xs));
+      }
+      if (++xs == P.xs) {
+        xs = 0;
+        xpar ^= 1u;
+      }
     }
+    // the sums are complete, and no MMA is under way when TMEM is freed
+    if (leader) tc::mma_commit(done_bar);
+    __syncwarp();
+    tc::mbar_wait(done_bar, 0, nullptr, tc::kDrainWaitNs);
   } else if (warp >= 4) {
     // -------------------------------------------------------------------- split
     // this thread's 16 bytes of each half of a tile (row r of 128 bytes, piece p),
@@ -246,18 +271,19 @@ __global__ void __launch_bounds__(few32::NT, 1) k_ffn_few32(const __grid_constan
     const int to0 = MN ? k * 128 + ((((r >> 5) * 4 + (p >> 1)) ^ (k & 7)) << 4) + (p & 1) * 8
                        : r * 64 + (((p >> 1) ^ ((r >> 1) & 3)) << 4) + (p & 1) * 8;
     for (int it = 0; it < blocks; ++it) {
-      const int rs = it % P.raws, s = it & 1;
-      bool ok = tc::mbar_pipe_wait<false>(raw_full(rs), (uint32_t)(it / P.raws) & 1u, abort_flag,
-                                          P.wait_ns);
-      if (ok && it >= 2)
-        ok = tc::mbar_pipe_wait<false>(set_empty(s), ((uint32_t)(it / 2) & 1u) ^ 1u, abort_flag,
-                                       P.wait_ns);
-      if (!ok && !*abort_flag) give_up();
-      if (!__all_sync(0xffffffffu, ok)) break;  // a warp leaves as one
+      const int s = it & 1;
+      bool ok = it < 2 || tc::mbar_pipe_wait<false>(set_empty(s), ((uint32_t)(it / 2) & 1u) ^ 1u,
+                                                    abort_flag, P.wait_ns);
 #pragma unroll
       for (int i = 0; i < NW; ++i) {
-        const uint8_t* src = smem + (rs * NW + i) * RAW;
-        uint8_t* dst = sets + s * set_bytes + i * 3 * PLANE;
+        const int n = it * NW + i, rs = n % P.raws;
+        ok = ok && tc::mbar_pipe_wait<false>(raw_full(rs), (uint32_t)(n / P.raws) & 1u, abort_flag,
+                                             P.wait_ns);
+        if (!ok && !*abort_flag) give_up();
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;  // a warp leaves as one
+        const uint8_t* src = smem + rs * RAW;
+        uint8_t* dst = sets + s * SETB + i * 3 * PLANE;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           uint2 h, m, l;
@@ -269,13 +295,13 @@ __global__ void __launch_bounds__(few32::NT, 1) k_ffn_few32(const __grid_constan
           *reinterpret_cast<uint2*>(dst + PLANE + to) = m;
           *reinterpret_cast<uint2*>(dst + 2 * PLANE + to) = l;
         }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(raw_empty(rs));
       }
+      if (!ok) break;
       tc::fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        tc::mbar_arrive(set_full(s));
-        tc::mbar_arrive(raw_empty(rs));
-      }
+      if (lane == 0) tc::mbar_arrive(set_full(s));
     }
   }
   __syncthreads();
@@ -428,11 +454,22 @@ cudaError_t launch(Few32P& P, const FewArgs& f, int64_t K, cudaStream_t s) {
   P.sets = sets_of(f.t, NW);
   P.tmem_cols = 32;
   while (P.tmem_cols < (uint32_t)(NW * P.sets * P.orders * P.np)) P.tmem_cols *= 2;
-  const int sets = 2 * (NW * 3 * PLANE + 3 * P.np * TK * 2);
-  P.raws = (ROOM - sets) / (NW * RAW);
-  if (P.raws > MAXRAW) P.raws = MAXRAW;
-  // the parts take the stages' place: NW np 512 bytes, less than the two sets
-  const int stage = sets + P.raws * NW * RAW;
+  // What the planes leave is shared out between the weights' ring and the tokens':
+  // a weight tile takes about 1.5 us from HBM and is free once split, a tokens' block
+  // 1 us from the L2 and is free a block or two later, after its MMAs.
+  const int sets = 2 * NW * 3 * PLANE, xbytes = 3 * P.np * TK * 2;
+  int most = 0;
+  for (int xs = 2; xs <= MAXX && ROOM - sets - xs * xbytes >= NW * RAW; ++xs) {
+    const int fit = (ROOM - sets - xs * xbytes) / RAW, raws = fit < MAXRAW ? fit : MAXRAW;
+    const int w = 2 * (2 * raws - NW), x = 3 * NW * (2 * xs - 3), score = w < x ? w : x;
+    if (score > most) {
+      most = score;
+      P.xs = xs;
+      P.raws = raws;
+    }
+  }
+  // the parts take the stages' place: NW np 512 bytes, less than the rings and planes
+  const int stage = P.raws * RAW + sets + P.xs * xbytes;
   const int64_t tiles = (P.rows + TM - 1) / TM, slots = sm_count();
   const int nk = P.nseg * P.kblocks;
   int parts = 0;
