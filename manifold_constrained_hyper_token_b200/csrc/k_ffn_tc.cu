@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(ftc::Cfg<TN, F32, more_warps(E, F32)>::NT, 1)
   const uint32_t mempty = tc::smem_u32(bars + 2 * NS + 4);  // fp32: the lower planes' sums
   const uint32_t fin_bar = tc::smem_u32(bars + 2 * NS + 5);
 
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const int rank = (int)tc::cluster_rank();
   const int64_t pair = blockIdx.x / 2, npairs = gridDim.x / 2;
   const int64_t tiles = (int64_t)P.mt * P.nt * P.nz * P.split;
@@ -306,64 +306,80 @@ __global__ void __launch_bounds__(ftc::Cfg<TN, F32, more_warps(E, F32)>::NT, 1)
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA
-    if (lane == 0 && rank == 0) {
+    // The warp waits together and elects the lane that issues, so that descriptors
+    // stay uniform; made up for a single lane they took longer than an MMA of N = 128.
+    if (rank == 0) {
       constexpr uint32_t idesc = tc::idesc_bf16(TM, TN, AMN, BMN);
-      int64_t it = 0;
+      const bool leader = tc::elect_one();
+      const uint32_t base0 = tc::smem_u32(smem);
+      auto wait_all = [&](auto wait) {
+        if (__all_sync(0xffffffffu, wait())) return true;
+        if (lane == 0) give_up();
+        return false;
+      };
+      int s = 0;
+      uint32_t par = 0;
       int n = 0;  // accumulators filled so far
       bool ok = true, any = false;
       uint32_t done = 0;  // tiles
       for (int64_t id = pair; id < tiles && ok; id += npairs, ++done) {
-        if (F32 && done > 0 &&
-            !tc::mbar_pipe_wait<true>(mempty, (done & 1u) ^ 1u, abort_flag, P.wait_ns)) {
-          give_up();
+        if (F32 && done > 0 && !wait_all([&] {
+              return tc::mbar_pipe_wait<true>(mempty, (done & 1u) ^ 1u, abort_flag, P.wait_ns);
+            }))
           break;
-        }
         int z, mi, ni, ja, jb;
         tile_at(P, id, z, mi, ni, ja, jb);
         for (int j0 = ja, j1; j0 < jb && ok; j0 = j1, ++n) {
           j1 = stay_end<F32>(j0, jb);
           const int buf = n & 1;
-          if (n >= 2 && !tc::mbar_pipe_wait<true>(tempty(buf), ((uint32_t)(n / 2) & 1u) ^ 1u,
-                                                  abort_flag, P.wait_ns)) {
-            give_up();
+          if (n >= 2 && !wait_all([&] {
+                return tc::mbar_pipe_wait<true>(tempty(buf), ((uint32_t)(n / 2) & 1u) ^ 1u,
+                                                abort_flag, P.wait_ns);
+              })) {
             ok = false;
             break;
           }
           tc::tc_fence_after();
-          for (int j = j0; j < j1; ++j, ++it) {
-            const int s = (int)(it % NS);
-            if (!tc::mbar_pipe_wait<false>(full(s), (uint32_t)(it / NS) & 1u, abort_flag,
-                                           P.wait_ns)) {
-              give_up();
+          for (int j = j0; j < j1; ++j) {
+            if (!wait_all([&] {
+                  return tc::mbar_pipe_wait<false>(full(s), par, abort_flag, P.wait_ns);
+                })) {
               ok = false;
               break;
             }
             tc::tc_fence_after();
-            const uint32_t base = tc::smem_u32(smem + s * STAGE);
+            const uint32_t base = base0 + s * STAGE;
             auto mma = [&](uint32_t col, int pa, int pb, int k, bool add) {
               tc::mma2_bf16(tmem + col, rows_desc<G, HALF, AMN>(base, pa, k),
                             rows_desc<G, HN, BMN>(base + G::ABYTES, pb, k), idesc, add ? 1u : 0u);
             };
+            if (leader) {
 #pragma unroll
-            for (int k = 0; k < TK / 16; ++k) {
-              if (F32) {
-                mma(G::MINOR, 2, 0, k, j > ja || k > 0);
-                mma(G::MINOR, 1, 1, k, true);
-                mma(G::MINOR, 0, 2, k, true);
-                mma(G::MINOR, 1, 0, k, true);
-                mma(G::MINOR, 0, 1, k, true);
+              for (int k = 0; k < TK / 16; ++k) {
+                if (F32) {
+                  mma(G::MINOR, 2, 0, k, j > ja || k > 0);
+                  mma(G::MINOR, 1, 1, k, true);
+                  mma(G::MINOR, 0, 2, k, true);
+                  mma(G::MINOR, 1, 0, k, true);
+                  mma(G::MINOR, 0, 1, k, true);
+                }
+                mma(buf * TN, 0, 0, k, j > j0 || k > 0);
               }
-              mma(buf * TN, 0, 0, k, j > j0 || k > 0);
+              tc::mma2_commit(empty(s));
             }
             any = true;
-            tc::mma2_commit(empty(s));
+            if (++s == NS) {
+              s = 0;
+              par ^= 1u;
+            }
           }
-          if (ok) tc::mma2_commit(tfull(buf));
+          if (ok && leader) tc::mma2_commit(tfull(buf));
         }
       }
       // every MMA issued here has finished before TMEM is freed
       if (any) {
-        tc::mma2_commit(fin_bar);
+        if (leader) tc::mma2_commit(fin_bar);
+        __syncwarp();
         tc::mbar_wait(fin_bar, 0, nullptr, tc::kDrainWaitNs);
       }
     }
