@@ -7,6 +7,35 @@
 
 namespace mhc {
 
+// Into how many parts (a cluster's CTAs) a sum of nk blocks of k is split, for `tiles`
+// row tiles and per_sm CTAs per SM; at least `least` parts.  A wave of CTAs takes
+// block_ns per block and what HBM needs to deliver one to each of them (2.5 ns per 16
+// KB of weights), and fixed_ns for its start and end.  kClusters: clusters of 1 to 8
+// CTAs that the machine holds at a time with one or two CTAs to an SM, a little below
+// what an empty one does (a cluster stays in one group of SMs, so that clusters of 8
+// leave 28 of 148 SMs idle, and a wave that filled the machine to the last place often
+// took two: T = 130, C = 7168, F = 14336 bf16, 159 us against 136).
+inline int split_sum(int64_t tiles, int64_t nk, int per_sm, int least, int tiles_16k,
+                     int64_t block_ns, int64_t fixed_ns) {
+  static constexpr int kClusters[2][8] = {{148, 74, 43, 32, 25, 21, 14, 14},
+                                          {296, 148, 89, 68, 53, 43, 35, 32}};
+  int parts = 0;
+  int64_t best = 0;
+  for (int p = least; p <= 8 && (p <= nk || p == least); ++p) {
+    const int64_t cl = kClusters[per_sm - 1][p - 1], blocks = (nk + p - 1) / p;
+    auto wave = [&](int64_t clusters) {
+      const int64_t hbm = clusters * p * tiles_16k * 5 / 2;
+      return clusters ? blocks * (block_ns + hbm) + fixed_ns : 0;
+    };
+    const int64_t cost = tiles / cl * wave(cl) + wave(tiles % cl);
+    if (parts == 0 || cost < best) {
+      best = cost;
+      parts = p;
+    }
+  }
+  return parts;
+}
+
 // Up to this many tokens the weights are the tall operand of the products.
 constexpr int64_t kFewTokens = 256;
 

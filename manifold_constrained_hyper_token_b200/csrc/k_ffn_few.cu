@@ -32,6 +32,7 @@ constexpr int NT = 128;
 constexpr int MAXST = 12;            // stages of the ring, at most
 constexpr int HALF_SMEM = 110 * 1024, FULL_SMEM = 222 * 1024;  // ring: two CTAs per SM, or one
 constexpr int TAIL = 1024 + 256;     // alignment, barriers
+constexpr int BLOCK_NS = 600, FIXED_NS = 4000;  // a k block; a CTA's start and end
 }  // namespace few
 
 enum FewEpi { FEW_STORE, FEW_GATE, FEW_DGATE };
@@ -297,14 +298,6 @@ cudaError_t token_map(CUtensorMap* m, const void* p, int64_t t, int64_t K, int p
   return make_tmap_bf16(m, p, 3, d, s, b, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-    return 148;
-  return n;
-}
-
 template <FewEpi E, bool MN> cudaError_t launch(FewP& P, const FewArgs& f, int64_t K, cudaStream_t s) {
   using namespace few;
   constexpr int NW = E == FEW_GATE ? 2 : 1;
@@ -322,19 +315,8 @@ template <FewEpi E, bool MN> cudaError_t launch(FewP& P, const FewArgs& f, int64
   P.stages = room / stage < MAXST ? room / stage : MAXST;
   const int ring = P.stages * stage;
   P.chunk = ring / (NW * TM * 4) / 16 * 16;
-  // the split of k: as many rounds over the machine as CTAs need, each with a k
-  // block's time per block and about six more for its start and its end
-  const int64_t tiles = (P.rows + TM - 1) / TM, slots = (int64_t)sm_count() * per_sm;
-  const int nk = P.nseg * P.kblocks;
-  int parts = 1;
-  int64_t best = 0;
-  for (int p = 1; p <= 8 && p <= nk; p *= 2) {
-    const int64_t cost = ((tiles * p + slots - 1) / slots) * ((nk + p - 1) / p + 6);
-    if (p == 1 || cost < best) {
-      best = cost;
-      parts = p;
-    }
-  }
+  const int64_t tiles = (P.rows + TM - 1) / TM;
+  const int parts = split_sum(tiles, P.nseg * P.kblocks, per_sm, 1, NW, BLOCK_NS, FIXED_NS);
   auto kern = k_ffn_few<E, MN>;
   const int smem = ring + TAIL;
   TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));

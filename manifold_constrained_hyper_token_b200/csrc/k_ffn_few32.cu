@@ -39,6 +39,7 @@ constexpr int PLANE = TM * TK * 2;    // ... one of its planes
 constexpr int NT = 640, NCONV = 16;   // threads; splitting warps
 constexpr int MAXRAW = 12, MAXX = 6;  // ring stages, at most: weight tiles, k blocks of tokens
 constexpr int ROOM = 222 * 1024, TAIL = 1024 + 512;
+constexpr int BLOCK_NS = 450, FIXED_NS = 5000;  // a weight tile; a CTA's start and end
 constexpr int kMaxK = 2048, kGoodK = 512;  // k per set of accumulators: at most; aimed at
 static_assert(RAW / 2 == 32 * NCONV * 16, "a thread takes 16 bytes of each half of a tile");
 }  // namespace few32
@@ -424,14 +425,6 @@ cudaError_t token_map(CUtensorMap* m, const void* p, int64_t t, int64_t K, int p
   return make_tmap_bf16(m, p, 3, d, s, b, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-    return 148;
-  return n;
-}
-
 int tokens16(int64_t t) { return (int)((t + 15) / 16 * 16); }
 
 // Accumulators per set, and sets per weight, of a product with nw weights.
@@ -470,19 +463,10 @@ cudaError_t launch(Few32P& P, const FewArgs& f, int64_t K, cudaStream_t s) {
   }
   // the parts take the stages' place: NW np 512 bytes, less than the rings and planes
   const int stage = P.raws * RAW + sets + P.xs * xbytes;
-  const int64_t tiles = (P.rows + TM - 1) / TM, slots = sm_count();
-  const int nk = P.nseg * P.kblocks;
-  int parts = 0;
-  int64_t best = 0;
-  for (int p = 1; p <= 8 && p <= nk; p *= 2) {
-    if ((int64_t)(nk + p - 1) / p * TK > (int64_t)kGoodK * P.sets && p < 8 && 2 * p <= nk)
-      continue;
-    const int64_t cost = ((tiles * p + slots - 1) / slots) * ((nk + p - 1) / p + 6);
-    if (parts == 0 || cost < best) {
-      best = cost;
-      parts = p;
-    }
-  }
+  const int64_t tiles = (P.rows + TM - 1) / TM;
+  const int nk = P.nseg * P.kblocks, good = kGoodK / TK * P.sets;
+  const int want = (nk + good - 1) / good, least = want < 8 ? want : 8;
+  const int parts = split_sum(tiles, nk, 1, least, NW, BLOCK_NS * NW, FIXED_NS);
   auto kern = k_ffn_few32<E, MN>;
   const int smem = stage + TAIL;
   TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));

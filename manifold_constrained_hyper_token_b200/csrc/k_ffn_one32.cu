@@ -2,8 +2,8 @@
 // cores: plain fp32 multiply-adds, bound by reading the weights once.  Eight tokens
 // take eight multiply-adds per weight, 16 weights a cycle and SM, against 5.8 that
 // memory delivers (6.55 TB/s over 148 SMs).  Forward, C = 7168, F = 14336: 217 us
-// with one token (5.7 TB/s), 244 with 4, 324 with 8; a variant for 16, whose sums
-// leave one CTA per SM, took 809 us, the tensor cores (k_ffn_few32.cu) 540.
+// with one token (5.7 TB/s), 241 with 4, 341 with 8; a variant for 16, whose sums
+// leave one CTA per SM, took 809 us, the tensor cores (k_ffn_few32.cu) 407.
 //
 // k_rows: weights stored along k (forward).  A warp takes four rows, its lanes
 // along k, and a row's tokens are reduced over the lanes at the end.
@@ -290,29 +290,8 @@ __global__ void __launch_bounds__(NTHR) k_cols(const __grid_constant__ OneP P) {
   if (P.beside) tc::grid_wait();
 }
 
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-    return 148;
-  return n;
-}
-
-// The split of k: two CTAs per SM want work; a chunk costs a chunk, a CTA's start
-// and end about four.
-int parts_of(int64_t tiles, int64_t chunks) {
-  const int64_t slots = 2 * sm_count();
-  int parts = 1;
-  int64_t best = 0;
-  for (int p = 1; p <= 8 && p <= chunks; p *= 2) {
-    const int64_t cost = ((tiles * p + slots - 1) / slots) * ((chunks + p - 1) / p + 4);
-    if (p == 1 || cost < best) {
-      best = cost;
-      parts = p;
-    }
-  }
-  return parts;
-}
+// The split of k: a chunk of either kernel is 32 KB of weights.
+int parts_of(int64_t tiles, int64_t chunks) { return split_sum(tiles, chunks, 2, 1, 2, 500, 3000); }
 
 template <OneEpi E, int TT> cudaError_t rows_tt(OneP& P, cudaStream_t s) {
   const int64_t tile = E == ONE_GATE ? NWARP * RPW / 2 : NWARP * RPW;
