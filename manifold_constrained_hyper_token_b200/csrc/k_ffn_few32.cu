@@ -8,12 +8,10 @@
 // the weights beforehand, as the products of many tokens do, would move 16 bytes
 // per weight instead of 4.
 //
-// A small MMA takes about as long as one of N = 128, so the tokens' planes lie one
-// after the other as one operand of 3 np rows, and three MMAs per 16 k do for six:
-//   W1 [X1 X2 X3] -> [D0 D1 D2],  W2 [X1 X2] -> [D1 D2],  W3 [X1] -> [D2]
-// with one accumulator D_o per order o (T = 1, C = 7168, F = 14336: 540 us with six).
-// Beyond 80 tokens N and TMEM do not hold that; there the six go to two
-// accumulators, orders 1 and 2 together.
+// X1 W1 has an accumulator of its own, the five smaller products share one.  (Three
+// accumulators, one per order, and three MMAs over the stacked planes [X1 X2 X3],
+// [X1 X2] and [X1] leave TMEM for fewer sets, and so force shorter parts: T = 64,
+// C = 4096, F = 4736, 132 us against 104; T = 17, C = 7168, F = 14336, 441 against 409.)
 //
 // The tensor cores' adder cuts instead of rounding, so a long sum is spread over up
 // to four sets of accumulators in turn and over the cluster, kGoodK per set where
@@ -50,7 +48,7 @@ struct Few32P {
   CUtensorMap w[2], x;
   int nseg, kblocks;
   int np, raws, xs;        // tokens rounded up to 16; weight tiles and token blocks on their way
-  int sets, orders;        // accumulator sets of a weight; accumulators in a set (3, or 2)
+  int sets;                // sets of two accumulators of a weight
   int64_t rows, t;
   void* o0;                // STORE: fp32 [t][rows]; else bf16 planes [3 or 6][t][rows]
   float *g, *u;            // GATE: kept unless null; DGATE: read
@@ -202,9 +200,8 @@ __global__ void __launch_bounds__(few32::NT, 1) k_ffn_few32(const __grid_constan
     // the lane that issues, which makes them uniform (T = 17, C = 7168, F = 14336:
     // 633 us as a single lane's loop, 562 with the descriptors prepared, 441 so)
     const bool leader = tc::elect_one();
-    const uint32_t np = (uint32_t)P.np, weight = (uint32_t)(P.sets * P.orders) * np;
-    const uint32_t id1 = tc::idesc_bf16(TM, P.np, MN, false);
-    const uint32_t idn = (np >> 3) << 17;  // one more np in N
+    const uint32_t np = (uint32_t)P.np, weight = (uint32_t)(2 * P.sets) * np;
+    const uint32_t idesc = tc::idesc_bf16(TM, P.np, MN, false);
     const uint64_t adesc = MN ? tc::smem_desc(tc::smem_u32(sets), PLANE / 2, 1024, tc::SWZ_128B)
                               : tc::smem_desc(tc::smem_u32(sets), 16, 512, tc::SWZ_64B);
     const uint64_t bdesc = tc::smem_desc(tc::smem_u32(xring), 16, 512, tc::SWZ_64B);
@@ -232,19 +229,14 @@ __global__ void __launch_bounds__(few32::NT, 1) k_ffn_few32(const __grid_constan
               const uint64_t a = a0 + (uint32_t)((i * 3 + pw) * (PLANE / 16) + k * (MN ? 128 : 2));
               const uint64_t b = b0 + (uint32_t)(k * 2);
               const uint32_t d = acc + i * weight;
-              if (P.orders == 3) {
-                // X1 .. X(3 - pw), into the orders from pw on
-                tc::mma_bf16(d + pw * np, a, b, id1 + (2 - pw) * idn, pw > 0 ? 1u : add);
-              } else {
 #pragma unroll
-                for (int px = 0; px < 3 - pw; ++px)
-                  tc::mma_bf16(d + (pw + px > 0 ? np : 0), a, b + (uint32_t)px * np * 4, id1,
-                               pw > 0 || px > 1 ? 1u : add);
-              }
+              for (int px = 0; px < 3 - pw; ++px)
+                tc::mma_bf16(d + (pw + px > 0 ? np : 0), a, b + (uint32_t)px * np * 4, idesc,
+                             pw > 0 || px > 1 ? 1u : add);
             }
           }
         }
-        acc += (uint32_t)P.orders * np;
+        acc += 2 * np;
         if (++set == P.sets) {
           set = 0;
           acc = tmem;
@@ -313,15 +305,15 @@ __global__ void __launch_bounds__(few32::NT, 1) k_ffn_few32(const __grid_constan
   if (warp < 4) {
     const int r = threadIdx.x;
     const uint32_t ta = tmem + ((uint32_t)(32 * warp) << 16);
-    // the lowest orders first, set by set
+    // the smaller products first, set by set
     const int steps = blocks * (TK / 16), used = steps < P.sets ? steps : P.sets;
 #pragma unroll
     for (int i = 0; i < NW; ++i)
       for (int c = 0; c < P.np; c += 16) {
         float v[16] = {}, m[16];
-        for (int o = P.orders - 1; o >= 0; --o)
+        for (int o = 1; o >= 0; --o)
           for (int q = 0; q < used; ++q) {
-            tc::tmem_get16(ta + ((i * P.sets + q) * P.orders + o) * P.np + c, m);
+            tc::tmem_get16(ta + ((i * P.sets + q) * 2 + o) * P.np + c, m);
 #pragma unroll
             for (int e = 0; e < 16; ++e) v[e] += m[e];
           }
@@ -427,10 +419,9 @@ cudaError_t token_map(CUtensorMap* m, const void* p, int64_t t, int64_t K, int p
 
 int tokens16(int64_t t) { return (int)((t + 15) / 16 * 16); }
 
-// Accumulators per set, and sets per weight, of a product with nw weights.
-int orders_of(int64_t t, int nw) { return 3 * tokens16(t) * nw <= 512 && t <= 80 ? 3 : 2; }
+// Sets of two accumulators per weight, of a product with nw weights.
 int sets_of(int64_t t, int nw) {
-  const int n = 512 / (nw * orders_of(t, nw) * tokens16(t));
+  const int n = 512 / (nw * 2 * tokens16(t));
   return n < 4 ? n : 4;
 }
 
@@ -443,10 +434,9 @@ cudaError_t launch(Few32P& P, const FewArgs& f, int64_t K, cudaStream_t s) {
   P.status = f.st;
   P.wait_ns = tc::wait_limit(f.wait_ns);
   P.kblocks = (int)((K + TK - 1) / TK);
-  P.orders = orders_of(f.t, NW);
   P.sets = sets_of(f.t, NW);
   P.tmem_cols = 32;
-  while (P.tmem_cols < (uint32_t)(NW * P.sets * P.orders * P.np)) P.tmem_cols *= 2;
+  while (P.tmem_cols < (uint32_t)(NW * P.sets * 2 * P.np)) P.tmem_cols *= 2;
   // What the planes leave is shared out between the weights' ring and the tokens':
   // a weight tile takes about 1.5 us from HBM and is free once split, a tokens' block
   // 1 us from the L2 and is free a block or two later, after its MMAs.
