@@ -216,10 +216,12 @@ __global__ void __launch_bounds__(ftc::Cfg<TN, F32, more_warps(E, F32)>::NT, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~(uintptr_t)1023);
-  // full[NS] empty[NS] tfull[2] tempty[2] mempty fin
+  // full[NS] empty[NS] tfull[2] tempty[2] mempty fin, the TMEM address and the abort
+  // flag, the stages that this CTA's copies were issued for
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + G::BAR_OFF);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * NS + 6);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile uint64_t* issued = reinterpret_cast<volatile uint64_t*>(bars + 2 * NS + 7);
   auto full = [&](int s) { return tc::smem_u32(bars + s); };
   auto empty = [&](int s) { return tc::smem_u32(bars + NS + s); };
   auto tfull = [&](int b) { return tc::smem_u32(bars + 2 * NS + b); };
@@ -303,6 +305,7 @@ __global__ void __launch_bounds__(ftc::Cfg<TN, F32, more_warps(E, F32)>::NT, 1)
           }
         }
       }
+      *issued = (uint64_t)it;
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA
@@ -320,7 +323,7 @@ __global__ void __launch_bounds__(ftc::Cfg<TN, F32, more_warps(E, F32)>::NT, 1)
       int s = 0;
       uint32_t par = 0;
       int n = 0;  // accumulators filled so far
-      bool ok = true, any = false;
+      bool ok = true;
       uint32_t done = 0;  // tiles
       for (int64_t id = pair; id < tiles && ok; id += npairs, ++done) {
         if (F32 && done > 0 && !wait_all([&] {
@@ -367,7 +370,6 @@ __global__ void __launch_bounds__(ftc::Cfg<TN, F32, more_warps(E, F32)>::NT, 1)
               }
               tc::mma2_commit(empty(s));
             }
-            any = true;
             if (++s == NS) {
               s = 0;
               par ^= 1u;
@@ -377,11 +379,9 @@ __global__ void __launch_bounds__(ftc::Cfg<TN, F32, more_warps(E, F32)>::NT, 1)
         }
       }
       // every MMA issued here has finished before TMEM is freed
-      if (any) {
-        if (leader) tc::mma2_commit(fin_bar);
-        __syncwarp();
-        tc::mbar_wait(fin_bar, 0, nullptr, tc::kDrainWaitNs);
-      }
+      if (leader) tc::mma2_commit(fin_bar);
+      __syncwarp();
+      tc::mbar_wait(fin_bar, 0, nullptr, tc::kDrainWaitNs);
     }
   } else if (warp >= 4) {
     // ----------------------------------------------------------- epilogue
@@ -580,12 +580,21 @@ __global__ void __launch_bounds__(ftc::Cfg<TN, F32, more_warps(E, F32)>::NT, 1)
   __syncthreads();
   tc::cluster_sync();  // no arrival or MMA of the partner is under way any more
   // After an ordinary run the MMAs have waited for every copy.  When either CTA gave
-  // up, copies may be on their way that no barrier of the first CTA counts any more
-  // (the two need not have issued the same ones): a millisecond, a thousand times
-  // what a copy takes, and both are done.
+  // up, copies may still be on their way, and the two need not have issued the same
+  // ones.  A CTA is at most a ring ahead (a stage is refilled once the MMAs have read
+  // both CTAs' copies in it), so each barrier has one open phase at most: the first
+  // CTA settles what was never issued and waits for the rest.
   if (*abort_flag) {  // of both CTAs, or of neither
-    const uint64_t t0 = tc::global_ns();
-    while (tc::global_ns() - t0 < 1000000) {
+    if (rank == 0 && threadIdx.x == 0) {
+      const uint64_t mine = *issued, other = tc::ld_cluster_u64(tc::map_cta(
+                                         tc::smem_u32(bars + 2 * NS + 7), 1));
+      const uint64_t most = mine > other ? mine : other;
+      for (uint64_t i = most > NS ? most - NS : 0; i < most; ++i) {
+        const uint32_t bar = full((int)(i % NS));
+        if (i >= mine) tc::mbar_arrive_expect_tx(bar, STAGE);  // the partner's copies alone
+        if (i >= other) tc::mbar_complete_tx(bar, STAGE);      // ... which do not come
+        tc::mbar_wait(bar, (uint32_t)(i / NS) & 1u, nullptr, tc::kDrainWaitNs);
+      }
     }
     __syncwarp();
     tc::cluster_sync();

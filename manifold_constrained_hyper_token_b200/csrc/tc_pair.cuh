@@ -51,6 +51,11 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                : "memory");
 }
+// Take `bytes` that will not come off what the current phase waits for.
+__device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
 // One try on phase `parity`.  CLUSTER: the barrier has arrivals from the partner
 // CTA, whose writes before them are visible from here.
 template <bool CLUSTER> __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
@@ -202,6 +207,12 @@ __device__ __forceinline__ void tmem_put16(uint32_t taddr, const float (&v)[16])
 // A word into the cluster's shared memory (an address from map_cta).
 __device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+// Eight bytes of the cluster's shared memory (an address from map_cta).
+__device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t addr) {
+  uint64_t v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+  return v;
 }
 // Four floats of the cluster's shared memory (an address from map_cta).
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {

@@ -240,6 +240,28 @@ def test_times_out_then_recovers(mhc, T, C, F, backward, dtype):
         _check_fwd(y, x, wg, wu, wd, "silu", dtype)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_gives_up_wherever_the_limit_falls(mhc, dtype):
+    """Limits from one clock to about a copy's time stop the paired products at stages that
+    differ from CTA to CTA.  Each call ends well inside the half second that a wait for a copy
+    which never comes would take, and leaves nothing behind for the next."""
+    x, wg, wu, wd, gy = _case(1500, 1032, 2056, dtype, 17)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    want = mhc.mhc_ffn(x, wg, wu, wd), *mhc.mhc_ffn_backward(x, wg, wu, wd, gy)
+    for limit in (1, 50, 150, 300, 600, 1000, 2000, 4000, 8000, 20000, 1000000):
+        begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        st.zero_()
+        begin.record()
+        mhc.mhc_ffn(x, wg, wu, wd, dev_status=st, wait_ns=limit)
+        mhc.mhc_ffn_backward(x, wg, wu, wd, gy, dev_status=st, wait_ns=limit)
+        end.record()
+        end.synchronize()
+        assert int(st.item()) in ((TIMEOUT,) if limit == 1 else (0, TIMEOUT))
+        assert begin.elapsed_time(end) < 250, limit
+        got = mhc.mhc_ffn(x, wg, wu, wd), *mhc.mhc_ffn_backward(x, wg, wu, wd, gy)
+        assert all(torch.equal(a, b) for a, b in zip(want, got)), limit
+
+
 @pytest.mark.parametrize("T", [3, 40, 300])
 def test_powers_of_two_pass_through(mhc, T):
     """fp32: x scaled by 2^-90 and both projections by 2^90 give the very bits of the unscaled
