@@ -8,8 +8,15 @@
 // HBM bound: one read of every input and one write of every output.  A token's
 // row stays on the chip between its statistics and its outputs.  Each warp takes
 // its own share of a row in two passes (its sum, then the squares about its own
-// mean), and the shares are joined as M2 = sum_w (M2_w + n_w (m_w - mean)^2): no
-// difference of large sums, and one block barrier per row.
+// mean m_w), and the shares are joined about the first warp's mean m_0:
+//   mean = m_0 + 1/C sum_w (n_w (m_w - m_0) + r_w),  r_w = sum of x - m_w
+//   M2   = sum_w (M2_w + d_w (2 r_w + n_w d_w)),     d_w = m_w - mean
+// No difference of large sums, one block barrier per row, and a mean that is off by
+// one rounding of itself where the row's values are close to one another: there s
+// is as large as 1/sqrt(eps) and would make every further rounding of the mean (of
+// a sum, a quotient, or of mean s in x s - mean s) part of the result.  r_w is what
+// is left of the warp's own roundings; in bf16 the sums of such rows are exact and
+// n_w m_w - sum gives it, in fp32 it is added up beside the squares.
 //
 // What is left to care about is the number of instructions: with 16 channels per
 // thread and a row at a time the shuffles and joins of a row cost more than its
@@ -83,11 +90,20 @@ __device__ __forceinline__ void load_param(const float* p, uint64_t (&v)[P]) {
   }
 }
 
-// What one warp knows of its share of a row: the mean of its channels, the squares
-// about that mean and, in the backward, the sums of a and of a (x - m).
+// What one warp knows of its share of a row: the mean of its channels as rounded, the
+// sum r and the squares of what is left about it and, in the backward, the sums of a
+// and of a (x - m).
 struct Share {
-  float m, m2, a, ax;
+  float m, m2, a, ax, r;
 };
+
+// The squares about the mean of n values whose squares about m are m2 and whose sum
+// about m is r, d = m - mean.  Roundings may leave it below zero.
+__device__ __forceinline__ float about_mean(float m2, float r, float n, float d) {
+  return fmaf(d, fmaf(n, d, 2.0f * r), m2);
+}
+// ... and 0 then; NaN stays.
+__device__ __forceinline__ float not_below_0(float v) { return v < 0.f ? 0.f : v; }
 
 // s is 0 only where the variance left fp32's range.
 __device__ __forceinline__ void report(float mean, float s, int* status) {
@@ -127,6 +143,15 @@ __device__ __forceinline__ float half_sum(float v) {
   return v;
 }
 
+// xh from d = x - m_w, the warp's own mean.  fp32: shift = m_w - mean, and d + shift is
+// exact for values near one another, where m_w is a few roundings off.  bf16: their m_w
+// is off by its own rounding only, and shift = (m_w - mean) s is no larger than the
+// largest xh, so that its rounding is 2^-24 of that.
+template <bool F32>
+__device__ __forceinline__ uint64_t from_share(uint64_t d, uint64_t shift, uint64_t s) {
+  return F32 ? f2mul(f2add(d, shift), s) : f2fma(d, s, shift);
+}
+
 // ------------------------------------------------------------------ forward
 // WARP: one row per warp (blockDim.x / 32 rows per CTA); otherwise one row per
 // CTA.  A thread holds VPT 16-byte vectors of its row.
@@ -136,8 +161,9 @@ __global__ void __launch_bounds__(MAXT)
                const float* __restrict__ w, const float* __restrict__ b, T* __restrict__ y,
                int* status) {
   constexpr int N = Vec<T>::N, P = Pairs<T>::P;
+  constexpr bool F32 = sizeof(T) == 4;
   using PV = Pairs<T>;
-  __shared__ float3 rec[16];
+  __shared__ float4 rec[16];
   const int tpr = WARP ? 32 : blockDim.x;
   const int t = WARP ? threadIdx.x % 32 : threadIdx.x;
   const int64_t row = WARP ? (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32
@@ -162,30 +188,35 @@ __global__ void __launch_bounds__(MAXT)
     }
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const float n = WARP ? (float)C : share_channels(warp, tpr, N, nvec);
-  float m = warp_sum(f2sum(sum)) * inv_or_0(n);
-  uint64_t m2 = 0, nm = f2dup(-m);
+  const float all = warp_sum(f2sum(sum)), mw = all * inv_or_0(n);
+  uint64_t m2 = 0, left = 0, nm = f2dup(-mw);
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
     if (t + i * tpr < nvec) {
 #pragma unroll
       for (int e = 0; e < P; ++e) {
-        const uint64_t d = f2add(v[i][e], nm);
+        const uint64_t d = v[i][e] = f2add(v[i][e], nm);
         m2 = f2fma(d, d, m2);
+        if (F32) left = f2add(left, d);
       }
     }
-  float var = warp_sum(f2sum(m2));
+  float var = warp_sum(f2sum(m2)), m;
+  const float r = F32 ? warp_sum(f2sum(left)) : fmaf(-n, mw, all);
   const float inv_c = 1.0f / (float)C;
-  if (!WARP) {
-    if (lane == 0) rec[warp] = make_float3(n, m, var);
+  if (WARP) {
+    m = fmaf(r, inv_c, mw);
+    var = about_mean(var, r, n, mw - m);
+  } else {
+    if (lane == 0) rec[warp] = make_float4(n, mw, var, r);
     __syncthreads();
-    const float3 q = lane < tpr / 32 ? rec[lane] : make_float3(0.f, 0.f, 0.f);
-    m = warp_sum(q.x * q.y) * inv_c;
-    const float d = q.y - m;
-    var = warp_sum(q.z + q.x * d * d);
+    const float4 q = lane < tpr / 32 ? rec[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float m0 = rec[0].y;
+    m = fmaf(warp_sum(fmaf(q.x, q.y - m0, q.w)), inv_c, m0);
+    var = warp_sum(about_mean(q.z, q.w, q.x, q.y - m));
   }
-  const float s = rsqrtf(var * inv_c + eps);
+  const float s = rsqrtf(not_below_0(var) * inv_c + eps);
   if (t == 0) report(m, s, status);
-  const uint64_t ss = f2dup(s), nms = f2dup(-m * s);
+  const uint64_t ss = f2dup(s), shift = f2dup(F32 ? mw - m : (mw - m) * s);
   uint4* yr = reinterpret_cast<uint4*>(y + row * C);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
@@ -196,7 +227,7 @@ __global__ void __launch_bounds__(MAXT)
       if (b) load_param<P>(b + (int64_t)k * N, bv);
 #pragma unroll
       for (int e = 0; e < P; ++e)
-        o[e] = f2fma(f2fma(v[i][e], ss, nms), wv[e], bv[e]);
+        o[e] = f2fma(from_share<F32>(v[i][e], shift, ss), wv[e], bv[e]);
       __stcs(yr + k, PV::pack(o));
     }
   }
@@ -212,8 +243,10 @@ __global__ void __launch_bounds__(MAXT, PERSM)
                      const float* __restrict__ w, const float* __restrict__ b, T* __restrict__ y,
                      int* status) {
   constexpr int N = Vec<T>::N, P = Pairs<T>::P;
+  constexpr bool F32 = sizeof(T) == 4;
   using PV = Pairs<T>;
-  __shared__ float2 rec[WARP ? 1 : 2][2][16];
+  constexpr int W = WARP ? 1 : MAXT / 32;
+  __shared__ float4 rec[WARP ? 1 : 2][2][W];
   extern __shared__ uint4 ring[];  // [group][2][row][nvec]
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int tpr = WARP ? 32 : blockDim.x;
@@ -223,7 +256,7 @@ __global__ void __launch_bounds__(MAXT, PERSM)
   uint4* mine = ring + (int64_t)g * 4 * nvec;
   const int64_t row0 = 2 * ((int64_t)blockIdx.x * per + g), step = 2 * (int64_t)gridDim.x * per;
   const float inv_c = 1.0f / (float)C;
-  const float inv_n = WARP ? inv_c : inv_or_0(share_channels(warp, tpr, N, nvec));
+  const float n = WARP ? (float)C : share_channels(warp, tpr, N, nvec), inv_n = inv_or_0(n);
   const float nq =
       WARP || (lane & 15) >= tpr / 32 ? 0.f : share_channels(lane & 15, tpr, N, nvec);
   tc::grid_wait();
@@ -265,10 +298,10 @@ __global__ void __launch_bounds__(MAXT, PERSM)
       }
     }
     // from here to the join a lane's scalars are its half-warp's row's
-    float m = pair_sum(f2sum(sum[0]), f2sum(sum[1]), lane) * inv_n;
-    const uint64_t nm[2] = {f2dup(-__shfl_sync(0xffffffffu, m, 0)),
-                            f2dup(-__shfl_sync(0xffffffffu, m, 16))};
-    uint64_t m2[2] = {0, 0};
+    const float all = pair_sum(f2sum(sum[0]), f2sum(sum[1]), lane), mw = all * inv_n;
+    const uint64_t nm[2] = {f2dup(-__shfl_sync(0xffffffffu, mw, 0)),
+                            f2dup(-__shfl_sync(0xffffffffu, mw, 16))};
+    uint64_t m2[2] = {0, 0}, left[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       if (t + i * tpr < nvec) {
@@ -276,27 +309,35 @@ __global__ void __launch_bounds__(MAXT, PERSM)
         for (int r = 0; r < 2; ++r)
 #pragma unroll
           for (int e = 0; e < P; ++e) {
-            const uint64_t d = f2add(v[r][i][e], nm[r]);
+            const uint64_t d = v[r][i][e] = f2add(v[r][i][e], nm[r]);
             m2[r] = f2fma(d, d, m2[r]);
+            if (F32) left[r] = f2add(left[r], d);
           }
       }
     }
-    float v2 = pair_sum(f2sum(m2[0]), f2sum(m2[1]), lane);
-    if (!WARP) {
-      if ((lane & 15) == 0) rec[it & 1][lane >> 4][warp] = make_float2(m, v2);
+    float v2 = pair_sum(f2sum(m2[0]), f2sum(m2[1]), lane), m;
+    const float rw =
+        F32 ? pair_sum(f2sum(left[0]), f2sum(left[1]), lane) : fmaf(-n, mw, all);
+    if (WARP) {
+      m = fmaf(rw, inv_c, mw);
+      v2 = about_mean(v2, rw, n, mw - m);
+    } else {
+      if ((lane & 15) == 0) rec[it & 1][lane >> 4][warp] = make_float4(mw, v2, rw, 0.f);
       __syncthreads();
-      const float2 q = nq > 0.f ? rec[it & 1][lane >> 4][lane & 15] : make_float2(0.f, 0.f);
-      m = half_sum(nq * q.x) * inv_c;
-      const float d = q.x - m;
-      v2 = half_sum(q.y + nq * d * d);
+      const float4* recs = rec[it & 1][lane >> 4];
+      const float4 q = nq > 0.f ? recs[lane & 15] : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float m0 = recs[0].x;
+      m = fmaf(half_sum(fmaf(nq, q.x - m0, q.z)), inv_c, m0);
+      v2 = half_sum(about_mean(q.y, q.z, nq, q.x - m));
     }
-    const float s = rsqrtf(v2 * inv_c + eps);
+    const float s = rsqrtf(not_below_0(v2) * inv_c + eps);
     if (t == 0 || (t == 16 && two)) report(m, s, status);
-    uint64_t ss[2], nms[2];
+    const float off = F32 ? mw - m : (mw - m) * s;
+    uint64_t ss[2], shift[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       ss[r] = f2dup(__shfl_sync(0xffffffffu, s, 16 * r));
-      nms[r] = f2dup(__shfl_sync(0xffffffffu, -m * s, 16 * r));
+      shift[r] = f2dup(__shfl_sync(0xffffffffu, off, 16 * r));
     }
     uint4* yr = reinterpret_cast<uint4*>(y + row * C);
 #pragma unroll
@@ -312,7 +353,7 @@ __global__ void __launch_bounds__(MAXT, PERSM)
             uint64_t o[P];
 #pragma unroll
             for (int e = 0; e < P; ++e)
-              o[e] = f2fma(f2fma(v[r][i][e], ss[r], nms[r]), wv[e], bv[e]);
+              o[e] = f2fma(from_share<F32>(v[r][i][e], shift[r], ss[r]), wv[e], bv[e]);
             __stcs(yr + r * nvec + k, PV::pack(o));
           }
         }
@@ -322,22 +363,24 @@ __global__ void __launch_bounds__(MAXT, PERSM)
 }
 
 // A row's statistics from its warps' shares, for CTAs of kMaxThreads.
-__device__ __forceinline__ Share join_shares(float n, const Share& mine, float4* rec, float* cnt,
+__device__ __forceinline__ Share join_shares(float n, const Share& mine, float4* rec, float2* cnt,
                                              int64_t C) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (lane == 0) {
     rec[warp] = make_float4(mine.m, mine.m2, mine.a, mine.ax);
-    cnt[warp] = n;
+    cnt[warp] = make_float2(n, mine.r);
   }
   __syncthreads();
   const float4 q = rec[lane];
-  const float nq = cnt[lane];
+  const float2 c = cnt[lane];
+  const float m0 = rec[0].x;
   Share r;
-  r.m = warp_sum(nq * q.x) / (float)C;
+  r.m = m0 + warp_sum(fmaf(c.x, q.x - m0, c.y)) / (float)C;
   const float d = q.x - r.m;
-  r.m2 = warp_sum(q.y + nq * d * d);
+  r.m2 = not_below_0(warp_sum(about_mean(q.y, c.y, c.x, d)));
   r.a = warp_sum(q.z);
   r.ax = warp_sum(q.w + d * q.z);
+  r.r = 0.f;
   return r;
 }
 
@@ -348,7 +391,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_fwd_long(
     const float* __restrict__ b, T* __restrict__ y, int* status) {
   constexpr int N = Vec<T>::N;
   __shared__ float4 rec[32];
-  __shared__ float num[32];
+  __shared__ float2 num[32];
   const int64_t row = blockIdx.x, nvec = C / N;
   const T* xr = x + row * C;
   float sum = 0.f, v[N];
@@ -364,15 +407,21 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_fwd_long(
   Share sh = {};
   const float n = warp_sum((float)cnt);
   sh.m = warp_sum(sum) * inv_or_0(n);
-  float m2 = 0.f;
+  float m2 = 0.f, left = 0.f;
   for (int64_t k = threadIdx.x; k < nvec; k += blockDim.x) {
     Vec<T>::load(xr + k * N, v);
-    float q = 0.f;
+    float q = 0.f, l = 0.f;
 #pragma unroll
-    for (int e = 0; e < N; ++e) q = fmaf(v[e] - sh.m, v[e] - sh.m, q);
+    for (int e = 0; e < N; ++e) {
+      const float d = v[e] - sh.m;
+      q = fmaf(d, d, q);
+      l += d;
+    }
     m2 += q;
+    left += l;
   }
   sh.m2 = warp_sum(m2);
+  sh.r = warp_sum(left);
   sh = join_shares(n, sh, rec, num, C);
   const float s = rsqrtf(sh.m2 / (float)C + eps);
   if (threadIdx.x == 0) report(sh.m, s, status);
@@ -402,8 +451,11 @@ __global__ void __launch_bounds__(MAXT, PERSM)
                const float* __restrict__ w, const T* __restrict__ gy, T* __restrict__ gx,
                float* __restrict__ part, int* status) {
   constexpr int N = Vec<T>::N, P = Pairs<T>::P;
+  constexpr bool F32 = sizeof(T) == 4;
   using PV = Pairs<T>;
-  __shared__ float4 rec[WARP ? 1 : 2][2][16];
+  constexpr int W = WARP ? 1 : MAXT / 32;
+  __shared__ float4 rec[WARP ? 1 : 2][2][W];
+  __shared__ float res[WARP ? 1 : 2][2][W];
   extern __shared__ uint4 ring[];  // [group][2][row][x, gy][nvec]; WARP, at the end: [2][C]
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int tpr = WARP ? 32 : blockDim.x;
@@ -414,7 +466,7 @@ __global__ void __launch_bounds__(MAXT, PERSM)
   const int64_t row0 = 2 * ((int64_t)blockIdx.x * per + g), step = 2 * (int64_t)gridDim.x * per;
   const float inv_c = 1.0f / (float)C;
   // this warp's channels, and those of the warp whose record this lane joins
-  const float inv_n = WARP ? inv_c : inv_or_0(share_channels(warp, tpr, N, nvec));
+  const float n = WARP ? (float)C : share_channels(warp, tpr, N, nvec), inv_n = inv_or_0(n);
   const float nq =
       WARP || (lane & 15) >= tpr / 32 ? 0.f : share_channels(lane & 15, tpr, N, nvec);
   tc::grid_release();
@@ -466,10 +518,10 @@ __global__ void __launch_bounds__(MAXT, PERSM)
       }
     }
     // from here to the join a lane's scalars are its half-warp's row's
-    float m = pair_sum(f2sum(sum[0]), f2sum(sum[1]), lane) * inv_n;
-    uint64_t nm[2] = {f2dup(-__shfl_sync(0xffffffffu, m, 0)),
-                      f2dup(-__shfl_sync(0xffffffffu, m, 16))};
-    uint64_t m2[2] = {0, 0}, sa[2] = {0, 0}, sax[2] = {0, 0};
+    const float all = pair_sum(f2sum(sum[0]), f2sum(sum[1]), lane), mw = all * inv_n;
+    uint64_t nm[2] = {f2dup(-__shfl_sync(0xffffffffu, mw, 0)),
+                      f2dup(-__shfl_sync(0xffffffffu, mw, 16))};
+    uint64_t m2[2] = {0, 0}, sa[2] = {0, 0}, sax[2] = {0, 0}, left[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int k = t + i * tpr;
@@ -485,30 +537,43 @@ __global__ void __launch_bounds__(MAXT, PERSM)
             m2[r] = f2fma(d, d, m2[r]);
             sa[r] = f2add(sa[r], a);
             sax[r] = f2fma(a, d, sax[r]);
+            if (F32) left[r] = f2add(left[r], d);
           }
         }
       }
     }
     float v2 = pair_sum(f2sum(m2[0]), f2sum(m2[1]), lane);
     float va = pair_sum(f2sum(sa[0]), f2sum(sa[1]), lane);
-    float vx = pair_sum(f2sum(sax[0]), f2sum(sax[1]), lane);
-    if (!WARP) {
-      if ((lane & 15) == 0) rec[it & 1][lane >> 4][warp] = make_float4(m, v2, va, vx);
+    float vx = pair_sum(f2sum(sax[0]), f2sum(sax[1]), lane), m;
+    const float rw =
+        F32 ? pair_sum(f2sum(left[0]), f2sum(left[1]), lane) : fmaf(-n, mw, all);
+    if (WARP) {
+      m = fmaf(rw, inv_c, mw);
+      const float d = mw - m;
+      v2 = about_mean(v2, rw, n, d);
+      vx = fmaf(d, va, vx);
+    } else {
+      if ((lane & 15) == 0) {
+        rec[it & 1][lane >> 4][warp] = make_float4(mw, v2, va, vx);
+        res[it & 1][lane >> 4][warp] = rw;
+      }
       __syncthreads();
-      const float4 q = nq > 0.f ? rec[it & 1][lane >> 4][lane & 15] : make_float4(0, 0, 0, 0);
-      m = half_sum(nq * q.x) * inv_c;
+      const float4* recs = rec[it & 1][lane >> 4];
+      const float4 q = nq > 0.f ? recs[lane & 15] : make_float4(0, 0, 0, 0);
+      const float qr = nq > 0.f ? res[it & 1][lane >> 4][lane & 15] : 0.f, m0 = recs[0].x;
+      m = fmaf(half_sum(fmaf(nq, q.x - m0, qr)), inv_c, m0);
       const float d = q.x - m;
-      v2 = half_sum(q.y + nq * d * d);
+      v2 = half_sum(about_mean(q.y, qr, nq, d));
       va = half_sum(q.z);
       vx = half_sum(q.w + d * q.z);
     }
-    const float s = rsqrtf(v2 * inv_c + eps);
+    const float s = rsqrtf(not_below_0(v2) * inv_c + eps);
     if (t == 0 || (t == 16 && two)) report(m, s, status);
     const float k1 = -va * inv_c, k2 = -vx * s * inv_c;
     uint64_t ss[2], c1[2], c2[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      nm[r] = f2dup(__shfl_sync(0xffffffffu, -m * s, 16 * r));
+      nm[r] = f2dup(-__shfl_sync(0xffffffffu, m, 16 * r));
       ss[r] = f2dup(__shfl_sync(0xffffffffu, s, 16 * r));
       c1[r] = f2dup(__shfl_sync(0xffffffffu, k1, 16 * r));
       c2[r] = f2dup(__shfl_sync(0xffffffffu, k2, 16 * r));
@@ -527,7 +592,7 @@ __global__ void __launch_bounds__(MAXT, PERSM)
             uint64_t o[P];
 #pragma unroll
             for (int e = 0; e < P; ++e) {
-              const uint64_t gv = PV::get(h, e), xh = f2fma(PV::get(q, e), ss[r], nm[r]);
+              const uint64_t gv = PV::get(h, e), xh = f2mul(f2add(PV::get(q, e), nm[r]), ss[r]);
               o[e] = f2mul(f2fma(xh, c2[r], f2fma(gv, wv[e], c1[r])), ss[r]);
               gw[i][e] = f2fma(gv, xh, gw[i][e]);
               gb[i][e] = f2add(gb[i][e], gv);
@@ -580,7 +645,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_bwd_long(
     const T* __restrict__ gy, T* __restrict__ gx, float2* __restrict__ stat, int* status) {
   constexpr int N = Vec<T>::N;
   __shared__ float4 rec[32];
-  __shared__ float num[32];
+  __shared__ float2 num[32];
   const int64_t row = blockIdx.x, nvec = C / N;
   float sum = 0.f, xv[N], gv[N];
   int64_t cnt = 0;
@@ -595,23 +660,26 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_bwd_long(
   Share sh = {};
   const float n = warp_sum((float)cnt);
   sh.m = warp_sum(sum) * inv_or_0(n);
-  float m2 = 0.f, sa = 0.f, sax = 0.f;
+  float m2 = 0.f, sa = 0.f, sax = 0.f, left = 0.f;
   for (int64_t k = threadIdx.x; k < nvec; k += blockDim.x) {
     Vec<T>::load(x + row * C + k * N, xv);
     Vec<T>::load(gy + row * C + k * N, gv);
-    float q2 = 0.f, qa = 0.f, qx = 0.f;
+    float q2 = 0.f, qa = 0.f, qx = 0.f, l = 0.f;
 #pragma unroll
     for (int e = 0; e < N; ++e) {
       const float d = xv[e] - sh.m, a = gv[e] * __ldg(w + k * N + e);
       q2 = fmaf(d, d, q2);
       qa += a;
       qx = fmaf(a, d, qx);
+      l += d;
     }
     m2 += q2;
     sa += qa;
     sax += qx;
+    left += l;
   }
   sh.m2 = warp_sum(m2);
+  sh.r = warp_sum(left);
   sh.a = warp_sum(sa);
   sh.ax = warp_sum(sax);
   sh = join_shares(n, sh, rec, num, C);
@@ -709,8 +777,8 @@ int64_t most_parts(int64_t rows, int64_t row_bytes) {
 }
 
 // CTAs of `threads` threads and `smem` bytes that an SM holds, at 128 registers a
-// thread (2 KB of shared memory beside: 1 KB of records, 1 KB of the system's), and
-// at most `most`.
+// thread (2 KB of shared memory beside: 1 KB for the records of 8 warps, 1 KB of the
+// system's), and at most `most`.
 int resident(int threads, size_t smem, int most) {
   const int by_regs = 512 / threads, by_smem = (int)(233472 / (smem + 2048));
   return std::max(1, std::min(most, std::min(by_regs, by_smem)));

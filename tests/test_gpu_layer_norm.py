@@ -85,6 +85,61 @@ def test_constant_rows(mhc, C):
     assert int(st.item()) == NONFINITE
 
 
+# a row per warp, per CTA, beyond the registers; pairs of rows (2368 bf16 rows and more), odd
+CLOSE = [(3, 72), (5, 264), (2, 520), (3, 1032), (2, 4104), (3, 7168), (2, 14344), (3, 16392),
+         (2369, 520), (2501, 1032), (2369, 7168)]
+
+
+@pytest.mark.parametrize("dtype,value", [(BF16, 3.0), (BF16, 7.0), (BF16, 100.0), (BF16, -100.5),
+                                         (F32, 7.0), (F32, 100.0), (F32, 100.1), (F32, 0.3)])
+@pytest.mark.parametrize("T,C", CLOSE)
+def test_rows_of_one_value(mhc, T, C, dtype, value):
+    """The mean of equal values is that value, whatever C is: y is the bias and grad_weight
+    zero to the bit although s is 1000, and without eps the row is reported."""
+    x = torch.full((T, C), value, dtype=dtype)
+    g = torch.Generator().manual_seed(C)
+    w, b = 1 + torch.rand(C, generator=g), torch.linspace(-1, 1, C)
+    gy = torch.randn(T, C, generator=g).to(dtype)
+    xd, wd, bd, gd = x.cuda(), w.cuda(), b.cuda(), gy.cuda()
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = mhc.mhc_layer_norm(xd, wd, bd, dev_status=st)
+    assert torch.equal(y.cpu(), b.to(dtype).expand(T, C))
+    gx, gw, _ = mhc.mhc_layer_norm_backward(xd, wd, gd, dev_status=st)
+    assert int(st.item()) == 0 and not bool(gw.any())
+    keep = slice(T - 3 if T > 3 else 0, T)
+    R.assert_within(gx[keep], R.norm_grad(x[keep], w, gy[keep], 1e-6)[0],
+                    R.norm_grad_bound(x[keep], w, gy[keep], 1e-6, dtype)[0], "grad_x")
+    for call in (lambda: mhc.mhc_layer_norm(xd, wd, bd, eps=0.0, dev_status=st),
+                 lambda: mhc.mhc_layer_norm_backward(xd, wd, gd, eps=0.0, dev_status=st)):
+        st.zero_()
+        call()
+        assert int(st.item()) == NONFINITE
+
+
+@pytest.mark.parametrize("dtype,value", [(BF16, 7.0), (BF16, 100.0), (F32, 100.0), (F32, 1000.1)])
+@pytest.mark.parametrize("T,C", CLOSE)
+def test_rows_of_nearly_one_value(mhc, T, C, dtype, value):
+    """One value in 50 a step of its type away, another value in each row.  The mean is rounded
+    once, u |mean|, which s (up to 1000) carries into every xh; the rounding also adds
+    (u mean)^2 to the variance, half of (s u mean)^2 of s.  All else is relative to xh: 64 u for
+    the variance's sum as elsewhere, 8 u for the square root, the difference and the product."""
+    g = torch.Generator().manual_seed(T + C)
+    x = (value * (1 + torch.arange(T) / T)).to(dtype)[:, None].repeat(1, C)
+    step = torch.finfo(dtype).eps * x.abs()
+    x = torch.where(torch.rand(T, C, generator=g) < 0.02, (x + step).to(dtype), x)
+    w, b = 1 + torch.rand(C, generator=g), torch.linspace(-1, 1, C)
+    y = mhc.mhc_layer_norm(x.cuda(), w.cuda(), b.cuda())
+    xd = x.double()
+    m = xd.mean(1, keepdim=True)
+    s = 1 / torch.sqrt(((xd - m) ** 2).mean(1, keepdim=True) + 1e-6)
+    xh = (xd - m) * s
+    dm = 1.01 * R.U * s * m.abs()
+    dxh = dm + (72 * R.U + dm * dm) * xh.abs()
+    ref = R.norm(x, w, b, 1e-6)
+    bound = w.double() * dxh + 4 * R.U * (ref.abs() + b.double().abs())
+    R.assert_within(y, ref, bound + R.HALF_STEP[dtype] * (ref.abs() + bound), "y")
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("C", [64, 1032, 40000])
