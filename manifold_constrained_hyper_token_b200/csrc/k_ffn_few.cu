@@ -318,9 +318,8 @@ template <FewEpi E, bool MN> cudaError_t launch(FewP& P, const FewArgs& f, int64
   const int64_t tiles = (P.rows + TM - 1) / TM;
   const int parts = split_sum(tiles, P.nseg * P.kblocks, per_sm, 1, NW, BLOCK_NS, FIXED_NS);
   auto kern = k_ffn_few<E, MN>;
-  const int smem = ring + TAIL;
-  TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  return launch_after(kern, (unsigned)(tiles * parts), NT, smem, (unsigned)parts, s, P);
+  TRY(allow_smem(kern, FULL_SMEM + TAIL));
+  return launch_after(kern, (unsigned)(tiles * parts), NT, ring + TAIL, (unsigned)parts, s, P);
 }
 
 FewP base(const FewArgs& f, int64_t rows, int nseg) {

@@ -458,9 +458,8 @@ cudaError_t launch(Few32P& P, const FewArgs& f, int64_t K, cudaStream_t s) {
   const int want = (nk + good - 1) / good, least = want < 8 ? want : 8;
   const int parts = split_sum(tiles, nk, 1, least, NW, BLOCK_NS * NW, FIXED_NS);
   auto kern = k_ffn_few32<E, MN>;
-  const int smem = stage + TAIL;
-  TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  return launch_after(kern, (unsigned)(tiles * parts), NT, smem, (unsigned)parts, s, P);
+  TRY(allow_smem(kern, ROOM + TAIL));
+  return launch_after(kern, (unsigned)(tiles * parts), NT, stage + TAIL, (unsigned)parts, s, P);
 }
 
 Few32P base(const FewArgs& f, int64_t rows, int nseg) {

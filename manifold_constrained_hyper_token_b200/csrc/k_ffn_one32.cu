@@ -302,10 +302,9 @@ template <OneEpi E, int TT> cudaError_t rows_tt(OneP& P, cudaStream_t s) {
 template <OneEpi E, int TT> cudaError_t cols_tt(OneP& P, cudaStream_t s) {
   const int64_t tiles = (P.rows + CTILE - 1) / CTILE;
   P.parts = parts_of(tiles, (P.K + CCHUNK - 1) / CCHUNK * P.nseg);
-  const size_t sm = (size_t)(2 * CCHUNK * TT + NWARP * TT * CTILE) * 4;
+  constexpr size_t sm = (size_t)(2 * CCHUNK * TT + NWARP * TT * CTILE) * 4;
   auto kern = k_cols<E, TT>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+  const cudaError_t e = allow_smem(kern, sm);
   if (e != cudaSuccess) return e;
   return launch_after(kern, (unsigned)(tiles * P.parts), NTHR, sm, (unsigned)P.parts, s, P);
 }

@@ -730,7 +730,7 @@ cudaError_t launch_tn(GemmArgs& P, const Opnds& o, cudaStream_t s) {
   P.mt = tiles_of(P.M, ftc::TM);
   P.nt = tiles_of(P.N, DUAL ? TN / 2 : TN);
   auto kern = k_ffn_tc<E, AMN, BMN, F32, TN>;
-  TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM));
+  TRY(allow_smem(kern, G::SMEM));
   const int64_t tiles = (int64_t)P.mt * P.nt * P.nz * P.split, pairs = sm_pairs();
   return launch_after(kern, (unsigned)(2 * (tiles < pairs ? tiles : pairs)), G::NT, G::SMEM, 2, s,
                       P);

@@ -792,8 +792,7 @@ cudaError_t fwd_pairs(int64_t rows, int64_t C, float eps, const T* x, const floa
   const int64_t groups = (rows + 2 * per - 1) / (2 * per);
   const int64_t g = (int64_t)sm_count() * resident(threads, sm, 8);
   auto kern = k_norm_fwd_pairs<T, VPT, WARP, MAXT, PERSM>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+  cudaError_t e = allow_smem(kern, 4 * MAXT * VPT * 16);
   if (e != cudaSuccess) return e;
   return launch_after(kern, (unsigned)(groups < g ? groups : g), (unsigned)threads, sm, 1, s, rows,
                       C, eps, x, w, b, y, st);
@@ -840,8 +839,7 @@ cudaError_t bwd_rows(int64_t rows, int64_t C, float eps, const T* x, const float
   const int64_t g = std::min<int64_t>(kMaxParts, (int64_t)sm_count() * resident(threads, sm, 4));
   *nparts = (int)(groups < g ? groups : g);  // at most most_parts()
   auto kern = k_norm_bwd<T, VPT, WARP, MAXT, PERSM>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+  cudaError_t e = allow_smem(kern, std::min<size_t>(8 * MAXT * VPT * 16, 4 * kLongRow));
   if (e != cudaSuccess) return e;
   return launch_after(kern, (unsigned)*nparts, (unsigned)threads, sm, 1, s, rows, C, eps, x, w, gy,
                       gx, part, st);

@@ -226,6 +226,14 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
 
 }  // namespace tc
 
+// Let a kernel take up to `most` bytes of dynamic shared memory.  The limit belongs to
+// the function in the whole process, so it is always the most that any of its launches
+// takes: a limit that went by the call would refuse the launch of another host thread
+// that is between these two calls.
+template <typename... P> cudaError_t allow_smem(void (*kern)(P...), size_t most) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+}
+
 // Launch with clusters of `cluster` CTAs whose set-up may run under the end of
 // the kernel before it (grid_wait holds the rest back).
 template <typename... P>
