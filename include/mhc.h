@@ -470,8 +470,9 @@ typedef struct mhc_ffn_params {
  * between the two matrix products.  With fp32 and more than 8 tokens the
  * products run on the tensor cores, each operand as the exact sum of three
  * bf16 numbers: relative to the sum of absolute products about 2^-24 from the
- * terms left out and 2^-19 from the adder over long sums; magnitudes below
- * 2^-110 lose bits.  A token that is not finite spoils its own row of y only.
+ * terms left out and 2^-19 from the adder, which cuts instead of rounding,
+ * whatever the sum's length (2^-18 for 9 to 128 tokens where C or F is above
+ * 8192); magnitudes below 2^-110 lose bits.  A token that is not finite spoils its own row of y only.
  * workspace: at least mhc_ffn_workspace_size(p) bytes, 256-byte aligned; its
  * contents on entry do not matter.  Repeated calls give identical bits.
  */

@@ -26,8 +26,10 @@
 // about half a unit of the last place per 16-wide step, which adds up over a long
 // sum (measured: 137 x 2^-24 at k = 5456).  So the first planes' products have
 // accumulators of their own, which they leave every kChunk k blocks to be added
-// up, rounded, in another TMEM region; the other products are 2^-8 of them and
-// less and stay in one accumulator to the end.
+// up, rounded, in another TMEM region.  The other products are 2^-7 of them and
+// less, five to each of theirs, and have one accumulator, which is emptied every
+// kMinor such stays: what it loses by then is about 2^-20 of the sum of absolute
+// products.  (Never emptied, it lost 2^-16.6 at k = 65536 and 2^-13.4 at 2^20.)
 //
 // The backward's g and u are kept in fp32: rounded to bf16 they would put as much
 // error into dg and du as these take from their own rounding.
@@ -53,6 +55,7 @@ constexpr int TM = 256;           // the pair's rows
 constexpr int HALF = 128;         // rows of A that one CTA brings
 constexpr int BAND = 8;
 constexpr int kChunk = 8;         // fp32: k blocks per stay of the first planes' products
+constexpr int kMinor = 16;        // ... and such stays per stay of the others'
 constexpr int BOX = 32 * 64;      // a staged box of results: 32 rows of 32 bf16 or 16 fp32
 
 template <int TN, bool F32, bool MORE> struct Cfg {
@@ -108,6 +111,11 @@ struct GemmArgs {
 // ends here.
 template <bool F32> __device__ __forceinline__ int stay_end(int j0, int jb) {
   return !F32 || jb - j0 < ftc::kChunk ? jb : j0 + ftc::kChunk;
+}
+
+// ... and with it that of the lower planes' products.
+__device__ __forceinline__ bool minor_end(int j1, int ja, int jb) {
+  return j1 == jb || (j1 - ja) % (ftc::kChunk * ftc::kMinor) == 0;
 }
 
 // A tile's place: plane z of the results (problem z / split, part z % split), row
@@ -324,17 +332,25 @@ __global__ void __launch_bounds__(ftc::Cfg<TN, F32, more_warps(E, F32)>::NT, 1)
       uint32_t par = 0;
       int n = 0;  // accumulators filled so far
       bool ok = true;
-      uint32_t done = 0;  // tiles
-      for (int64_t id = pair; id < tiles && ok; id += npairs, ++done) {
-        if (F32 && done > 0 && !wait_all([&] {
-              return tc::mbar_pipe_wait<true>(mempty, (done & 1u) ^ 1u, abort_flag, P.wait_ns);
-            }))
-          break;
+      uint32_t minors = 0;  // stays of the lower planes' products begun so far
+      for (int64_t id = pair; id < tiles && ok; id += npairs) {
         int z, mi, ni, ja, jb;
         tile_at(P, id, z, mi, ni, ja, jb);
+        int jm = ja;  // where the current one began
         for (int j0 = ja, j1; j0 < jb && ok; j0 = j1, ++n) {
           j1 = stay_end<F32>(j0, jb);
           const int buf = n & 1;
+          if (F32 && (j0 == ja || minor_end(j0, ja, jb))) {
+            jm = j0;
+            if (minors > 0 && !wait_all([&] {
+                  return tc::mbar_pipe_wait<true>(mempty, (minors & 1u) ^ 1u, abort_flag,
+                                                  P.wait_ns);
+                })) {
+              ok = false;
+              break;
+            }
+            ++minors;
+          }
           if (n >= 2 && !wait_all([&] {
                 return tc::mbar_pipe_wait<true>(tempty(buf), ((uint32_t)(n / 2) & 1u) ^ 1u,
                                                 abort_flag, P.wait_ns);
@@ -360,7 +376,7 @@ __global__ void __launch_bounds__(ftc::Cfg<TN, F32, more_warps(E, F32)>::NT, 1)
 #pragma unroll
               for (int k = 0; k < TK / 16; ++k) {
                 if (F32) {
-                  mma(G::MINOR, 2, 0, k, j > ja || k > 0);
+                  mma(G::MINOR, 2, 0, k, j > jm || k > 0);
                   mma(G::MINOR, 1, 1, k, true);
                   mma(G::MINOR, 0, 2, k, true);
                   mma(G::MINOR, 1, 0, k, true);
@@ -432,7 +448,8 @@ __global__ void __launch_bounds__(ftc::Cfg<TN, F32, more_warps(E, F32)>::NT, 1)
         tc::tc_fence_after();
         const uint32_t ta = tmem + ((uint32_t)(32 * q) << 16) + buf * TN;
         if (F32) {
-          // this stay's sums to those before it; at the end the lower planes' too
+          // this stay's sums to those before it; at their end the lower planes' too
+          const bool minor = minor_end(j1, ja, jb);
 #pragma unroll 1
           for (int c = 0; c < TN; c += 16) {
             float v[16], m[16];
@@ -443,7 +460,7 @@ __global__ void __launch_bounds__(ftc::Cfg<TN, F32, more_warps(E, F32)>::NT, 1)
 #pragma unroll
               for (int i = 0; i < 16; ++i) v[i] += m[i];
             }
-            if (j1 == jb) {
+            if (minor) {
               tc::tmem_get16(sums + c - G::SUMS + G::MINOR, m);
 #pragma unroll
               for (int i = 0; i < 16; ++i) v[i] += m[i];
@@ -454,7 +471,7 @@ __global__ void __launch_bounds__(ftc::Cfg<TN, F32, more_warps(E, F32)>::NT, 1)
           __syncwarp();
           if (lane == 0) {
             tc::mbar_arrive_cluster(tc::map_cta(tempty(buf), 0));
-            if (j1 == jb) tc::mbar_arrive_cluster(tc::map_cta(mempty, 0));
+            if (minor) tc::mbar_arrive_cluster(tc::map_cta(mempty, 0));
           }
         }
         if (j1 == jb) {

@@ -355,3 +355,78 @@ def test_long_sums_with_few_results(mhc, T, C, F, dtype):
     _check_bwd(got, x, wg, wu, wd, gy, "silu", dtype)
     again = mhc.mhc_ffn(x, wg, wu, wd), *mhc.mhc_ffn_backward(x, wg, wu, wd, gy)
     assert all(torch.equal(a, b) for a, b in zip((y, *got), again))
+
+
+# Sums of one sign, where a tensor-core adder that cuts is off in one direction.  A step of 16
+# products may cut twice, by up to 2^-23 of what is summed so far: half of k 2^-26 over a sum of
+# k equal terms, k 2^-27.
+def _positive(seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return lambda *s: torch.rand(*s, generator=g, device="cuda") * 0.5 + 0.5
+
+
+def _long_gate(mhc, T, C, dtype):
+    """y = a through a w_down that picks 64 hidden units, and a in fp64: the sums are over C."""
+    p = _positive(C)
+    x, wg, wu = p(T, C).to(dtype), (p(64, C) * 16 / C).to(dtype), (p(64, C) * 16 / C).to(dtype)
+    wd = torch.zeros(C, 64, dtype=dtype, device="cuda")
+    wd[:64] = torch.eye(64, device="cuda")
+    g = u = 0
+    for k in range(0, C, 1 << 15):
+        s = slice(k, k + (1 << 15))
+        g, u = g + x[:, s].double() @ wg[:, s].double().T, u + x[:, s].double() @ wu[:, s].double().T
+    return mhc.mhc_ffn(x, wg, wu, wd)[:, :64], R.gate(g, "silu")[0] * u
+
+
+def _long_weight_grads(mhc, T, C, F, dtype):
+    """grad_w_up and grad_w_down of 64 hidden units, and both in fp64: the sums are over T."""
+    p = _positive(T)
+    x, gy = p(T, C).to(dtype), p(T, C).to(dtype)
+    wg, wu, wd = (p(F, C) * 4 / C).to(dtype), (p(F, C) * 4 / C).to(dtype), (p(C, F) / F).to(dtype)
+    _, _, gwu, gwd = mhc.mhc_ffn_backward(x, wg, wu, wd, gy)
+    ru = rd = 0
+    for t in range(0, T, 1 << 13):
+        s = slice(t, t + (1 << 13))
+        _, _, u, d = R.ffn_grad(x[s], wg[:64], wu[:64], wd[:, :64], gy[s], "silu")
+        ru, rd = ru + u, rd + d
+    return (gwu[:64], ru), (gwd[:, :64], rd)
+
+
+def _off(got, ref):
+    """The mean of the relative differences: what all elements are off by together."""
+    return abs(float(((got.double() - ref) / ref).mean()))
+
+
+# fp32, k_ffn_tc: the first planes' sums leave their accumulator every 256 k, 2^-19; the others,
+# below 2^-6 of them together and in five products each, every 4096: 5 2^-15 2^-6 = 2^-18.7;
+# what is left out 2^-21; what is added in rounded steps does not lean to a side.
+FP32_SUM = 2.0 ** -19 + 5 * 2.0 ** -21 + 2.0 ** -21
+
+
+def test_long_fp32_sums_of_one_sign(mhc):
+    """a = silu(g) u takes the error of g (times at most 1.1 at g of 9) and that of u."""
+    for C in (4096, 65536, 131072):
+        assert _off(*_long_gate(mhc, 300, C, F32)) < 2.1 * FP32_SUM, C
+    for got, ref in _long_weight_grads(mhc, 131072, 1024, 2432, F32):
+        # the factors of the terms are themselves products: g, u and da over at most 1024
+        assert _off(got, ref) < (1 + 2.1) * FP32_SUM
+
+
+def test_few_token_fp32_sums_of_one_sign(mhc):
+    """k_ffn_few32 leaves up to 2048 k in an accumulator: 2^-16."""
+    for T, C in ((17, 32768), (100, 16384)):
+        assert _off(*_long_gate(mhc, T, C, F32)) < 2.1 * 2.0 ** -16, (T, C)
+
+
+@pytest.mark.parametrize("T,C,F", [(3, 4096, 8200), (17, 8192, 4096), (100, 4096, 8192),
+                                   (300, 8192, 4096), (4500, 1024, 2432)])
+def test_fp32_error_in_the_norm(mhc, T, C, F):
+    """The element bound grows with k and would let a lost plane pass; in the 2-norm the
+    roundings of a sum of k terms of either sign grow with its square root: 2^-19 (the adder, in
+    256 k) or 2^-16 (2048 k of k_ffn_few32), less than 2^-17 in fact, and two products in a row
+    with a factor each.  A lost second plane would be 2^-9."""
+    x, wg, wu, wd, gy = _case(T, C, F, F32, 18)
+    assert R.norm_rel(mhc.mhc_ffn(x, wg, wu, wd), R.ffn(x, wg, wu, wd, "silu")) < 2.0 ** -15
+    ref = R.ffn_grad(x, wg, wu, wd, gy, "silu")
+    for g, r, name in zip(mhc.mhc_ffn_backward(x, wg, wu, wd, gy), ref, GRADS):
+        assert R.norm_rel(g, r) < 2.0 ** -15, name
