@@ -36,6 +36,10 @@ inline int split_sum(int64_t tiles, int64_t nk, int per_sm, int least, int tiles
   return parts;
 }
 
+// bf16 sums longer than this are split (plan in k_ffn_tc.cu has the reason; over at most
+// eight parts for few tokens).
+constexpr int64_t kLongSum = 65536;
+
 // Up to this many tokens the weights are the tall operand of the products.
 constexpr int64_t kFewTokens = 256;
 

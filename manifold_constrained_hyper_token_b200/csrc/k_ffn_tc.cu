@@ -759,6 +759,11 @@ cudaError_t launch_tn(GemmArgs& P, const Opnds& o, cudaStream_t s) {
 // against 3.63 ms for the forward pass).  A plain result of few tiles and a long k
 // is also split along k, into parts of eight k blocks at least, where that saves 24
 // blocks of about a quarter of a microsecond: adding up the parts costs four.
+// bf16 sums of any number of tiles are split where they are longer than kLongSum:
+// they stay in one accumulator, whose adder cuts, and a sum of one sign is off by
+// 2^-11.8 of itself at 65536 k, a sixth of its rounding to bf16 (2^-8.2 at 2^19; fp32
+// sums leave the accumulator on their way).  The parts' fp32 planes are less than a
+// tenth of what g, u, dg, du and a take at such a length.
 struct Plan {
   int tn, split;
 };
@@ -774,6 +779,7 @@ Plan plan(bool f32, bool dual, bool plain, int64_t M, int64_t N, int nz, int64_t
     const int64_t s = std::min<int64_t>(std::min(pairs / tiles, nk / 8), 16);
     if (s > 1 && nk - nk / s >= 24) p.split = (int)s;
   }
+  if (plain && !f32) p.split = (int)std::max<int64_t>(p.split, (nk * 64 + kLongSum - 1) / kLongSum);
   return p;
 }
 size_t part_bytes(const Plan& p, int64_t M, int64_t N, int nz) {

@@ -379,9 +379,10 @@ def _long_gate(mhc, T, C, dtype):
 
 
 def _long_weight_grads(mhc, T, C, F, dtype):
-    """grad_w_up and grad_w_down of 64 hidden units, and both in fp64: the sums are over T."""
+    """grad_w_up and grad_w_down of 64 hidden units, and both in fp64: the sums are over T.  Each
+    channel has a factor of its own, so that the results do not all round the same way."""
     p = _positive(T)
-    x, gy = p(T, C).to(dtype), p(T, C).to(dtype)
+    x, gy = ((p(T, C) * 2 * p(1, C)).to(dtype) for _ in range(2))
     wg, wu, wd = (p(F, C) * 4 / C).to(dtype), (p(F, C) * 4 / C).to(dtype), (p(C, F) / F).to(dtype)
     _, _, gwu, gwd = mhc.mhc_ffn_backward(x, wg, wu, wd, gy)
     ru = rd = 0
@@ -410,6 +411,27 @@ def test_long_fp32_sums_of_one_sign(mhc):
     for got, ref in _long_weight_grads(mhc, 131072, 1024, 2432, F32):
         # the factors of the terms are themselves products: g, u and da over at most 1024
         assert _off(got, ref) < (1 + 2.1) * FP32_SUM
+
+
+def test_long_bf16_sums_of_one_sign(mhc):
+    """Sums over tokens and over hidden units are added up in fp32 from parts of 65536 terms:
+    65536 2^-27 (a quarter of a bf16 rounding), however long they are.  What else all elements
+    are off by together: the cuts in g, u and da over 1024 or 2048 channels, and the mean of as
+    many roundings to bf16 as there are elements (2^-9 over the square root of 8192)."""
+    own = 2.1 * 2048 * 2.0 ** -27 + 2 * 2.0 ** -9 / 8192 ** 0.5
+    for got, ref in _long_weight_grads(mhc, 262144, 1024, 2560, BF16):
+        assert _off(got, ref) < 2.0 ** -11 + own
+    # y over 2^18 hidden units: many row tiles, and few tokens
+    C, F = 2048, 262144
+    p = _positive(F)
+    wg, wu = (p(F, C) * 4 / C).to(BF16), (p(F, C) * 4 / C).to(BF16)
+    wd = (p(C, F) * p(C, 1) / F).to(BF16)
+    for T in (1300, 40):
+        x = p(T, C).to(BF16)
+        y = mhc.mhc_ffn(x, wg, wu, wd)[:4]
+        ref = sum(R.ffn(x[:4], wg[f:f + 4096], wu[f:f + 4096], wd[:, f:f + 4096], "silu")
+                  for f in range(0, F, 4096))
+        assert _off(y, ref) < 2.0 ** -11 + own, T
 
 
 def test_few_token_fp32_sums_of_one_sign(mhc):
