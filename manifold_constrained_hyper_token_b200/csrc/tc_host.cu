@@ -6,7 +6,7 @@
 
 #include <mutex>
 
-#include "tc_sm100.cuh"
+#include "tc_pair.cuh"
 
 namespace mhc {
 

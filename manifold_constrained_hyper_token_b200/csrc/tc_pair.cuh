@@ -226,6 +226,11 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
 
 }  // namespace tc
 
+// make_tmap_bf16 for any element type; box, swizzle and promotion as there.
+cudaError_t make_tmap(CUtensorMap* map, CUtensorMapDataType type, const void* base, int rank,
+                      const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
+                      CUtensorMapSwizzle swz, CUtensorMapL2promotion promo);
+
 // Let a kernel take up to `most` bytes of dynamic shared memory.  The limit belongs to
 // the function in the whole process, so it is always the most that any of its launches
 // takes: a limit that went by the call would refuse the launch of another host thread

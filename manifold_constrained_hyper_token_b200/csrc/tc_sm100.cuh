@@ -279,14 +279,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn = fals
 }  // namespace tc
 
 // ------------------------------------------------------------- host side
-// Encode a tiled TMA descriptor for a tensor of `rank` dims, bf16 or `type`
+// Encode a tiled TMA descriptor for a bf16 tensor of `rank` dims
 // (dims[0] innermost, strides_bytes[i] = byte stride of dim i+1).  `promo`
 // sets how much the L2 fill is widened around each requested row: rows that
 // the same CTA reads in full soon after (channel-chunked streams) profit from
 // 256 B, short rows whose neighbours are read much later want 64 B.
-cudaError_t make_tmap(CUtensorMap* map, CUtensorMapDataType type, const void* base, int rank,
-                      const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
-                      CUtensorMapSwizzle swz, CUtensorMapL2promotion promo);
 cudaError_t make_tmap_bf16(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                            const uint64_t* strides_bytes, const uint32_t* box,
                            CUtensorMapSwizzle swz,

@@ -102,6 +102,14 @@ def test_ncu_traffic_is_tied_to_the_kernel_sources(monkeypatch):
     assert bench.ncu_traffic("no_such_call") is None
 
 
+def test_ncu_traffic_of_the_measured_calls_is_current():
+    """The backward's figures were captured on the kernels as they are: a change that touches
+    only what other kernels use must not make them stale, and a change of theirs means a new
+    capture."""
+    for key in ("bwd_apply", "bwd_map"):
+        assert bench.ncu_traffic(key) is not None, key
+
+
 def _reference_line(*args, env=None):
     cmd = [sys.executable, os.path.join(ROOT, "bench.py"), "--impl", "reference",
            "--steps", "3", "--warmup", "1", "--reference-seconds", "2", *args]
