@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(few32::NT, 1) k_ffn_few32(const __grid_constan
     flag_status(P.status, MHC_ERR_TIMEOUT);
   };
 
-  // the weights' loader needs nothing from the kernel before this one
+  // the first ring of weights needs nothing from the kernel before this one
   if (P.beside) {
     tc::grid_release();
   } else if (warp != 0 || !P.early) {
@@ -149,6 +149,9 @@ __global__ void __launch_bounds__(few32::NT, 1) k_ffn_few32(const __grid_constan
       int it = 0;  // tiles: a k block has NW
       for (; it < blocks * NW; ++it) {
         const int s = it % P.raws;
+        // a tile is free once split, and the splitting warps wait for the kernel before
+        // this one: its time is not this wait's
+        if (P.early && it == P.raws) tc::grid_wait();
         if (it >= P.raws &&
             !tc::mbar_pipe_wait<false>(raw_empty(s), ((uint32_t)(it / P.raws) & 1u) ^ 1u,
                                        abort_flag, P.wait_ns)) {

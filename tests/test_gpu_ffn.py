@@ -240,6 +240,19 @@ def test_times_out_then_recovers(mhc, T, C, F, backward, dtype):
         _check_fwd(y, x, wg, wu, wd, "silu", dtype)
 
 
+@pytest.mark.parametrize("dtype,limit", [(F32, 40000), (BF16, 40000)])
+def test_the_kernel_before_is_no_wait(mhc, dtype, limit):
+    """The limit is for waits inside a kernel, on copies and on other warps: microseconds.  A few
+    tokens' down projection has its first weights on their way while the gate still runs, for
+    hundreds of microseconds here, and does not count that."""
+    x, wg, wu, wd, _ = _case(128, 7168, 14336, dtype, 19)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    want = mhc.mhc_ffn(x, wg, wu, wd)
+    for _ in range(5):
+        got = mhc.mhc_ffn(x, wg, wu, wd, dev_status=st, wait_ns=limit)
+        assert int(st.item()) == 0 and torch.equal(got, want)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_gives_up_wherever_the_limit_falls(mhc, dtype):
     """Limits from one clock to about a copy's time stop the paired products at stages that
