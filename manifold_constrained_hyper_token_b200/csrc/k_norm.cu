@@ -233,18 +233,17 @@ __global__ void __launch_bounds__(MAXT)
   }
 }
 
-// Many rows: persistent CTAs that take two rows at a time, as the backward does (see
+// Many bf16 rows: persistent CTAs that take two rows at a time, as the backward does (see
 // there), through a ring of two row pairs in shared memory.  Two rows share the
 // loads of weight and bias and half the shuffles, and a CTA's fixed work is paid
 // once: T = 16384, C = 7168 bf16 takes 98 us against 106 with a row per CTA.
-template <typename T, int VPT, bool WARP, int MAXT, int PERSM>
+template <int VPT, bool WARP, int MAXT, int PERSM>
 __global__ void __launch_bounds__(MAXT, PERSM)
-    k_norm_fwd_pairs(int64_t rows, int64_t C, float eps, const T* __restrict__ x,
-                     const float* __restrict__ w, const float* __restrict__ b, T* __restrict__ y,
-                     int* status) {
-  constexpr int N = Vec<T>::N, P = Pairs<T>::P;
-  constexpr bool F32 = sizeof(T) == 4;
-  using PV = Pairs<T>;
+    k_norm_fwd_pairs(int64_t rows, int64_t C, float eps, const __nv_bfloat16* __restrict__ x,
+                     const float* __restrict__ w, const float* __restrict__ b,
+                     __nv_bfloat16* __restrict__ y, int* status) {
+  using PV = Pairs<__nv_bfloat16>;
+  constexpr int N = Vec<__nv_bfloat16>::N, P = PV::P;
   constexpr int W = WARP ? 1 : MAXT / 32;
   __shared__ float4 rec[WARP ? 1 : 2][2][W];
   extern __shared__ uint4 ring[];  // [group][2][row][nvec]
@@ -301,7 +300,7 @@ __global__ void __launch_bounds__(MAXT, PERSM)
     const float all = pair_sum(f2sum(sum[0]), f2sum(sum[1]), lane), mw = all * inv_n;
     const uint64_t nm[2] = {f2dup(-__shfl_sync(0xffffffffu, mw, 0)),
                             f2dup(-__shfl_sync(0xffffffffu, mw, 16))};
-    uint64_t m2[2] = {0, 0}, left[2] = {0, 0};
+    uint64_t m2[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       if (t + i * tpr < nvec) {
@@ -311,13 +310,11 @@ __global__ void __launch_bounds__(MAXT, PERSM)
           for (int e = 0; e < P; ++e) {
             const uint64_t d = v[r][i][e] = f2add(v[r][i][e], nm[r]);
             m2[r] = f2fma(d, d, m2[r]);
-            if (F32) left[r] = f2add(left[r], d);
           }
       }
     }
     float v2 = pair_sum(f2sum(m2[0]), f2sum(m2[1]), lane), m;
-    const float rw =
-        F32 ? pair_sum(f2sum(left[0]), f2sum(left[1]), lane) : fmaf(-n, mw, all);
+    const float rw = fmaf(-n, mw, all);
     if (WARP) {
       m = fmaf(rw, inv_c, mw);
       v2 = about_mean(v2, rw, n, mw - m);
@@ -332,7 +329,7 @@ __global__ void __launch_bounds__(MAXT, PERSM)
     }
     const float s = rsqrtf(not_below_0(v2) * inv_c + eps);
     if (t == 0 || (t == 16 && two)) report(m, s, status);
-    const float off = F32 ? mw - m : (mw - m) * s;
+    const float off = (mw - m) * s;
     uint64_t ss[2], shift[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -353,7 +350,7 @@ __global__ void __launch_bounds__(MAXT, PERSM)
             uint64_t o[P];
 #pragma unroll
             for (int e = 0; e < P; ++e)
-              o[e] = f2fma(from_share<F32>(v[r][i][e], shift[r], ss[r]), wv[e], bv[e]);
+              o[e] = f2fma(from_share<false>(v[r][i][e], shift[r], ss[r]), wv[e], bv[e]);
             __stcs(yr + r * nvec + k, PV::pack(o));
           }
         }
@@ -784,14 +781,14 @@ int resident(int threads, size_t smem, int most) {
   return std::max(1, std::min(most, std::min(by_regs, by_smem)));
 }
 
-template <typename T, int VPT, bool WARP, int MAXT, int PERSM>
-cudaError_t fwd_pairs(int64_t rows, int64_t C, float eps, const T* x, const float* w,
-                      const float* b, T* y, int threads, int* st, cudaStream_t s) {
+template <int VPT, bool WARP, int MAXT, int PERSM>
+cudaError_t fwd_pairs(int64_t rows, int64_t C, float eps, const __nv_bfloat16* x, const float* w,
+                      const float* b, __nv_bfloat16* y, int threads, int* st, cudaStream_t s) {
   const int per = WARP ? threads / 32 : 1;
-  const size_t sm = (size_t)per * 4 * C * sizeof(T);
+  const size_t sm = (size_t)per * 4 * C * 2;
   const int64_t groups = (rows + 2 * per - 1) / (2 * per);
   const int64_t g = (int64_t)sm_count() * resident(threads, sm, 8);
-  auto kern = k_norm_fwd_pairs<T, VPT, WARP, MAXT, PERSM>;
+  auto kern = k_norm_fwd_pairs<VPT, WARP, MAXT, PERSM>;
   cudaError_t e = allow_smem(kern, 4 * MAXT * VPT * 16);
   if (e != cudaSuccess) return e;
   return launch_after(kern, (unsigned)(groups < g ? groups : g), (unsigned)threads, sm, 1, s, rows,
@@ -802,15 +799,16 @@ template <typename T>
 cudaError_t fwd(int64_t rows, int64_t C, float eps, const T* x, const float* w, const float* b,
                 T* y, int* st, cudaStream_t s) {
   const int64_t nvec = C / Vec<T>::N;
-  constexpr int V = 32 / Vec<T>::N;  // vectors of a thread
-  const int threads = round32((nvec + V - 1) / V);
   // fp32 rows have half the arithmetic per byte and run faster one to a CTA (T =
   // 8192, C = 4096: 49 us against 61)
-  if (sizeof(T) == 2 && rows >= 16 * sm_count()) {
-    if (C > 512 && C <= 1024)
-      return fwd_pairs<T, V, true, 128, 4>(rows, C, eps, x, w, b, y, 128, st, s);
-    if (C > 1024 && C <= 8192)
-      return fwd_pairs<T, V, false, 256, 2>(rows, C, eps, x, w, b, y, threads, st, s);
+  if constexpr (sizeof(T) == 2) {
+    if (rows >= 16 * sm_count()) {
+      const int threads = round32((nvec + 3) / 4);  // four vectors, 32 channels, to a thread
+      if (C > 512 && C <= 1024)
+        return fwd_pairs<4, true, 128, 4>(rows, C, eps, x, w, b, y, 128, st, s);
+      if (C > 1024 && C <= 8192)
+        return fwd_pairs<4, false, 256, 2>(rows, C, eps, x, w, b, y, threads, st, s);
+    }
   }
   if (nvec > 8 * 512) {
     k_norm_fwd_long<T><<<(unsigned)rows, kMaxThreads, 0, s>>>(C, eps, x, w, b, y, st);

@@ -58,6 +58,38 @@ def test_norm_backward(mhc, T, C, dtype):
     assert int(st.item()) == 0
 
 
+@pytest.mark.parametrize("T,C", [(2368, 1032), (2369, 520), (2400, 2048), (2501, 1024),
+                                 (2501, 1032), (2369, 4104), (2369, 7168), (2369, 8192),
+                                 (2369, 8200)])
+def test_many_rows(mhc, T, C):
+    """From 2368 bf16 rows on (16 to an SM) two rows go through a CTA or warp at a time: an odd
+    last row, one to eight warps to a row, a row that is not finite beside one that is, and rows
+    before and behind the output, which keep their bytes."""
+    x, w, b, _ = _case(T, C, BF16, T + C)
+    xd, wd, bd = x.cuda(), w.cuda(), b.cuda()
+    ref, bound = R.norm(x, w, b, 1e-6), R.norm_bound(x, w, b, 1e-6, BF16)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    first = None
+    for _ in range(2):
+        y = torch.full((T + 2, C), 7.0, dtype=BF16, device="cuda")
+        mhc.mhc_layer_norm(xd, wd, bd, out=y[1:-1], dev_status=st)
+        assert int(st.item()) == 0
+        assert bool((y[0] == 7).all()) and bool((y[-1] == 7).all())
+        assert first is None or torch.equal(first, y)
+        first = y
+    R.assert_within(y[1:-1], ref, bound, "y")
+    R.assert_within(mhc.mhc_layer_norm(xd, wd), R.norm(x, w, None, 1e-6),
+                    R.norm_bound(x, w, None, 1e-6, BF16), "y without bias")
+    for bad in (T - 1, T - 2, 0):
+        spoilt = xd.clone()
+        spoilt[bad, C - 1] = float("nan")
+        st.zero_()
+        got = mhc.mhc_layer_norm(spoilt, wd, bd, dev_status=st)
+        assert int(st.item()) == NONFINITE
+        keep = [t for t in range(T) if t != bad]
+        assert torch.equal(got[keep], y[1:-1][keep])
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("T,C", [(4, 64), (3, 2048), (2, 40000)])
 def test_rows_far_from_zero(mhc, T, C, dtype):
