@@ -319,6 +319,48 @@ def test_calls_on_two_streams_at_once(mhc):
             assert all(torch.equal(p, q) for p, q in zip(a, b))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,C,F", [(1, 1024, 2728), (5, 1024, 2728), (48, 1024, 2728),
+                                   (200, 1024, 2728), (300, 1024, 2728)])
+def test_weights_written_just_before_the_call(mhc, T, C, F, dtype):
+    """The later products of a call read their weights before the kernel ahead of them has ended;
+    a write of the weights that the stream has ahead of the call is seen all the same, by a copy
+    or by the library's own kernels, which let the next one start early."""
+    a = _case(T, C, F, dtype, 40)
+    sets = [a[1:4], _case(T, C, F, dtype, 41)[1:4]]
+    x, gy = a[0], a[4]
+    want = [(mhc.mhc_ffn(x, *w), *mhc.mhc_ffn_backward(x, *w, gy)) for w in sets]
+    w = [t.clone() for t in sets[0]]
+    got = []
+    for i in (1, 0, 1, 1, 0, 0, 1):
+        for order in ((0, 1, 2), (2, 1, 0)):
+            for k in order:
+                w[k].copy_(sets[i][k])
+            got.append((i, (mhc.mhc_ffn(x, *w),)))
+            for k in order:
+                w[k].copy_(sets[1 - i][k])
+            got.append((1 - i, (None, *mhc.mhc_ffn_backward(x, *w, gy))))
+    torch.cuda.synchronize()
+    for i, outs in got:
+        for p, q in zip(want[i], outs):
+            assert q is None or torch.equal(p, q)
+    # w_down and w_up as rows that the norm writes, the call's input from another call
+    ones = torch.ones(F, device="cuda"), torch.ones(C, device="cuda")
+    down, up = mhc.mhc_layer_norm(sets[1][2], ones[0]), mhc.mhc_layer_norm(sets[1][1], ones[1])
+    h = mhc.mhc_ffn(x, *sets[0])
+    torch.cuda.synchronize()
+    want = mhc.mhc_ffn(h, sets[0][0], up, down), *mhc.mhc_ffn_backward(h, sets[0][0], up, down, gy)
+    for _ in range(5):
+        h2, up2, down2 = (torch.full_like(t, float("nan")) for t in (h, up, down))
+        torch.cuda.synchronize()
+        mhc.mhc_ffn(x, *sets[0], out=h2)
+        mhc.mhc_layer_norm(sets[1][1], ones[1], out=up2)
+        mhc.mhc_layer_norm(sets[1][2], ones[0], out=down2)
+        got = (mhc.mhc_ffn(h2, sets[0][0], up2, down2),
+               *mhc.mhc_ffn_backward(h2, sets[0][0], up2, down2, gy))
+        assert all(torch.equal(p, q) for p, q in zip(want, got))
+
+
 def test_back_to_back_calls_share_a_workspace(mhc):
     """Calls on one stream with one workspace: each starts when the one before is done with it,
     although their kernels are set up early."""
