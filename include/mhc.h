@@ -415,8 +415,10 @@ typedef struct mhc_norm_params {
  *   out: y [T][C] (dtype)
  * dev_status gets MHC_ERR_NONFINITE when a token's mean or 1/sqrt(var + eps)
  * is not finite (a non-finite input, or a constant row with eps = 0) or the sum
- * of (x[c] - mean)^2 is above float32's largest value; only that token's row of y
- * is then undefined.  No workspace.
+ * of x[c] or of (x[c] - mean)^2 is above float32's largest value; only that
+ * token's row of y is then undefined.  No workspace.
+ * The mean is within one rounding of itself where the row's values are close to
+ * one another: equal values give y = bias exactly, whatever eps > 0 is.
  */
 MHC_API mhc_status mhc_layer_norm(const mhc_norm_params *p, const void *x, const float *weight,
                                   const float *bias, void *y, int *dev_status,

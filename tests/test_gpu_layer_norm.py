@@ -209,6 +209,22 @@ def test_squares_beyond_fp32_are_reported(mhc, T, C, dtype):
         R.assert_within(y[keep], R.norm(xs, w, b, 1e-6), R.norm_bound(xs, w, b, 1e-6, dtype), "y")
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,C", [(5, 1024), (5, 7168), (2501, 7168), (5, 40000)])
+def test_sums_beyond_fp32_are_reported(mhc, T, C, dtype):
+    """A row of 1e36 has a finite mean and no deviation, but its sum leaves fp32: it is reported
+    and stays alone."""
+    x, w, b, gy = _case(T, C, dtype, C)
+    x[T - 2] = 1e36
+    st = torch.zeros(2, dtype=torch.int32, device="cuda")
+    y = mhc.mhc_layer_norm(x.cuda(), w.cuda(), b.cuda(), dev_status=st[:1]).cpu()
+    mhc.mhc_layer_norm_backward(x.cuda(), w.cuda(), gy.cuda(), dev_status=st[1:])
+    assert st.tolist() == [NONFINITE, NONFINITE]
+    keep = [t for t in range(T) if t != T - 2]
+    R.assert_within(y[keep], R.norm(x[keep], w, b, 1e-6),
+                    R.norm_bound(x[keep], w, b, 1e-6, dtype), "y")
+
+
 @pytest.mark.parametrize("T,C", [(1000, 64), (777, 7168), (70, 40000)])
 def test_repeats_bit_for_bit_and_writes_nothing_else(mhc, T, C):
     x, w, b, gy = _case(T, C, BF16, 3)
