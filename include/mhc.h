@@ -475,10 +475,9 @@ typedef struct mhc_ffn_params {
  * terms left out and 2^-19 from the adder, which cuts instead of rounding,
  * whatever the sum's length (2^-18 for 9 to 128 tokens where C or F is above
  * 8192); magnitudes below 2^-110 lose bits.  bf16 sums stay in the adder for up to
- * 65536 terms (sums over F, and over T in mhc_ffn_backward; over C as long as C
- * is; with up to 256 tokens an eighth of the sum where that is more): 2^-11 of the
- * sum of absolute products there, in proportion for other lengths.  A token that
- * is not finite spoils its own row of y only.
+ * 65536 terms: 2^-11 of the sum of absolute products for those and longer ones, in
+ * proportion for shorter ones.  A token that is not finite spoils its own row of y
+ * only.
  * workspace: at least mhc_ffn_workspace_size(p) bytes, 256-byte aligned; its
  * contents on entry do not matter.  Repeated calls give identical bits.
  */

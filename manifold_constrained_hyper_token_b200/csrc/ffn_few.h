@@ -36,8 +36,8 @@ inline int split_sum(int64_t tiles, int64_t nk, int per_sm, int least, int tiles
   return parts;
 }
 
-// bf16 sums longer than this are split (plan in k_ffn_tc.cu has the reason; over at most
-// eight parts for few tokens).
+// bf16 sums longer than this do not stay in one accumulator (plan in k_ffn_tc.cu has the
+// reason).
 constexpr int64_t kLongSum = 65536;
 
 // Up to this many tokens the weights are the tall operand of the products.

@@ -316,9 +316,10 @@ template <FewEpi E, bool MN> cudaError_t launch(FewP& P, const FewArgs& f, int64
   const int ring = P.stages * stage;
   P.chunk = ring / (NW * TM * 4) / 16 * 16;
   const int64_t tiles = (P.rows + TM - 1) / TM;
-  const int64_t nk = (int64_t)P.nseg * P.kblocks, want = (nk * TK + kLongSum - 1) / kLongSum;
-  const int parts =
-      split_sum(tiles, nk, per_sm, want < 8 ? (int)want : 8, NW, BLOCK_NS, FIXED_NS);
+  // up to 8 kLongSum k come here
+  const int64_t nk = (int64_t)P.nseg * P.kblocks;
+  const int least = (int)((nk + kLongSum / TK - 1) / (kLongSum / TK));
+  const int parts = split_sum(tiles, nk, per_sm, least, NW, BLOCK_NS, FIXED_NS);
   auto kern = k_ffn_few<E, MN>;
   TRY(allow_smem(kern, FULL_SMEM + TAIL));
   return launch_after(kern, (unsigned)(tiles * parts), NT, ring + TAIL, (unsigned)parts, s, P);

@@ -31,6 +31,10 @@
 // kMinor such stays: what it loses by then is about 2^-20 of the sum of absolute
 // products.  (Never emptied, it lost 2^-16.6 at k = 65536 and 2^-13.4 at 2^20.)
 //
+// bf16 sums stay in one accumulator for up to kLongSum k: plain products are split
+// (plan), and the gate's and its derivative's over more channels (LONG) leave it as the
+// first planes' sums do.
+//
 // The backward's g and u are kept in fp32: rounded to bf16 they would put as much
 // error into dg and du as these take from their own rounding.
 //
@@ -109,8 +113,9 @@ struct GemmArgs {
 
 // The stay in an accumulator that starts at k block j0 of a tile that ends at jb
 // ends here.
-template <bool F32> __device__ __forceinline__ int stay_end(int j0, int jb) {
-  return !F32 || jb - j0 < ftc::kChunk ? jb : j0 + ftc::kChunk;
+template <bool F32, bool LONG> __device__ __forceinline__ int stay_end(int j0, int jb) {
+  constexpr int chunk = F32 ? ftc::kChunk : (int)(kLongSum / 64);
+  return !(F32 || LONG) || jb - j0 < chunk ? jb : j0 + chunk;
 }
 
 // ... and with it that of the lower planes' products.
@@ -214,11 +219,13 @@ __device__ __forceinline__ void row16(const float* base, int64_t row, int64_t co
   }
 }
 
-template <Epi E, bool AMN, bool BMN, bool F32, int TN>
-__global__ void __launch_bounds__(ftc::Cfg<TN, F32, more_warps(E, F32)>::NT, 1)
+template <Epi E, bool AMN, bool BMN, bool F32, int TN, bool LONG>
+__global__ void __launch_bounds__(ftc::Cfg<TN, F32, more_warps(E, F32 || LONG)>::NT, 1)
     k_ffn_tc(const __grid_constant__ GemmArgs P) {
   using namespace ftc;
-  using G = Cfg<TN, F32, more_warps(E, F32)>;
+  using G = Cfg<TN, F32, more_warps(E, F32 || LONG)>;
+  constexpr bool SUM = F32 || LONG;  // the results are sums of stays
+  static_assert(!SUM || 4 * TN <= 512, "TMEM columns");
   constexpr int NEPI = G::NEPI;
   constexpr int STAGE = G::STAGE, NS = G::NS, TK = G::TK, HN = TN / 2;
   extern __shared__ uint8_t smem_raw[];
@@ -338,7 +345,7 @@ __global__ void __launch_bounds__(ftc::Cfg<TN, F32, more_warps(E, F32)>::NT, 1)
         tile_at(P, id, z, mi, ni, ja, jb);
         int jm = ja;  // where the current one began
         for (int j0 = ja, j1; j0 < jb && ok; j0 = j1, ++n) {
-          j1 = stay_end<F32>(j0, jb);
+          j1 = stay_end<F32, LONG>(j0, jb);
           const int buf = n & 1;
           if (F32 && (j0 == ja || minor_end(j0, ja, jb))) {
             jm = j0;
@@ -439,7 +446,7 @@ __global__ void __launch_bounds__(ftc::Cfg<TN, F32, more_warps(E, F32)>::NT, 1)
         row16(P.u, row, (int64_t)ni * COLS + first, P.M, P.N, unext);
       }
       for (int j0 = ja, j1; j0 < jb; j0 = j1, ++n) {
-        j1 = stay_end<F32>(j0, jb);
+        j1 = stay_end<F32, LONG>(j0, jb);
         const int buf = n & 1;
         ok = tc::mbar_pipe_wait<false>(tfull(buf), (uint32_t)(n / 2) & 1u, abort_flag, tile_ns);
         if (!ok && !*abort_flag) give_up();
@@ -447,9 +454,9 @@ __global__ void __launch_bounds__(ftc::Cfg<TN, F32, more_warps(E, F32)>::NT, 1)
         if (!ok) break;
         tc::tc_fence_after();
         const uint32_t ta = tmem + ((uint32_t)(32 * q) << 16) + buf * TN;
-        if (F32) {
+        if (SUM) {
           // this stay's sums to those before it; at their end the lower planes' too
-          const bool minor = minor_end(j1, ja, jb);
+          const bool minor = F32 && minor_end(j1, ja, jb);
 #pragma unroll 1
           for (int c = 0; c < TN; c += 16) {
             float v[16], m[16];
@@ -475,7 +482,7 @@ __global__ void __launch_bounds__(ftc::Cfg<TN, F32, more_warps(E, F32)>::NT, 1)
           }
         }
         if (j1 == jb) {
-          const uint32_t at = F32 ? sums : ta;  // D's columns
+          const uint32_t at = SUM ? sums : ta;  // D's columns
 #pragma unroll 1
           for (int c = first; c < first + MINE; c += WIDE ? 64 : 32) {
             const int64_t col = (int64_t)ni * COLS + c;
@@ -583,7 +590,7 @@ __global__ void __launch_bounds__(ftc::Cfg<TN, F32, more_warps(E, F32)>::NT, 1)
             }
           }
         }
-        if (!F32) {
+        if (!SUM) {
           tc::tc_fence_before();
           __syncwarp();
           if (lane == 0) tc::mbar_arrive_cluster(tc::map_cta(tempty(buf), 0));
@@ -736,17 +743,17 @@ struct Opnds {
   int64_t K;
 };
 
-template <Epi E, bool AMN, bool BMN, bool F32, int TN>
+template <Epi E, bool AMN, bool BMN, bool F32, int TN, bool LONG = false>
 cudaError_t launch_tn(GemmArgs& P, const Opnds& o, cudaStream_t s) {
   constexpr bool DUAL = E == EPI_GATE || E == EPI_KEEP;
-  using G = ftc::Cfg<TN, F32, more_warps(E, F32)>;
+  using G = ftc::Cfg<TN, F32, more_warps(E, F32 || LONG)>;
   TRY(operand_map(&P.a, o.a, AMN, ftc::HALF, G::NP));
   TRY(operand_map(&P.b[0], o.b[0], BMN, G::BROWS, G::NP));
   if (o.b[1].p) TRY(operand_map(&P.b[1], o.b[1], BMN, G::BROWS, G::NP));
   P.kblocks = tiles_of(o.K, G::TK);
   P.mt = tiles_of(P.M, ftc::TM);
   P.nt = tiles_of(P.N, DUAL ? TN / 2 : TN);
-  auto kern = k_ffn_tc<E, AMN, BMN, F32, TN>;
+  auto kern = k_ffn_tc<E, AMN, BMN, F32, TN, LONG>;
   TRY(allow_smem(kern, G::SMEM));
   const int64_t tiles = (int64_t)P.mt * P.nt * P.nz * P.split, pairs = sm_pairs();
   return launch_after(kern, (unsigned)(2 * (tiles < pairs ? tiles : pairs)), G::NT, G::SMEM, 2, s,
@@ -791,13 +798,17 @@ cudaError_t launch(GemmArgs& P, const Opnds& o, int tn, cudaStream_t s) {
   if constexpr (F32) {
     return launch_tn<E, AMN, BMN, true, 128>(P, o, s);
   } else {
+    if constexpr (E == EPI_GATE || E == EPI_KEEP || E == EPI_DGATE) {
+      if (o.K > kLongSum) return launch_tn<E, AMN, BMN, false, 128, true>(P, o, s);
+    }
     return tn == 128 ? launch_tn<E, AMN, BMN, false, 128>(P, o, s)
                      : launch_tn<E, AMN, BMN, false, 256>(P, o, s);
   }
 }
 
 bool few_tokens(bool f32, int64_t t, int64_t C, int64_t F) {
-  return f32 ? t <= kOneTokens || few32_fits(t, C, F) : t <= kFewTokens;
+  if (f32) return t <= kOneTokens || few32_fits(t, C, F);
+  return t <= kFewTokens && std::max(C, 2 * F) <= 8 * kLongSum;  // a cluster's parts
 }
 
 // Operands as the products take them: the caller's bf16 arrays, or the split

@@ -421,9 +421,12 @@ def _positive(seed):
 
 
 def _long_gate(mhc, T, C, dtype):
-    """y = a through a w_down that picks 64 hidden units, and a in fp64: the sums are over C."""
+    """y = a through a w_down that picks 64 hidden units, and a in fp64: the sums are over C.
+    Tokens and hidden units have factors of their own (g is 4.5 to 18), so that the results do
+    not all round the same way."""
     p = _positive(C)
-    x, wg, wu = p(T, C).to(dtype), (p(64, C) * 16 / C).to(dtype), (p(64, C) * 16 / C).to(dtype)
+    x, wg = (p(T, C) * 2 * p(T, 1)).to(dtype), (p(64, C) * 16 / C).to(dtype)
+    wu = (p(64, C) * 2 * p(64, 1) * 16 / C).to(dtype)
     wd = torch.zeros(C, 64, dtype=dtype, device="cuda")
     wd[:64] = torch.eye(64, device="cuda")
     g = u = 0
@@ -460,7 +463,7 @@ FP32_SUM = 2.0 ** -19 + 5 * 2.0 ** -21 + 2.0 ** -21
 
 
 def test_long_fp32_sums_of_one_sign(mhc):
-    """a = silu(g) u takes the error of g (times at most 1.1 at g of 9) and that of u."""
+    """a = silu(g) u takes the error of g (times at most 1.1 for g above 4) and that of u."""
     for C in (4096, 65536, 131072):
         assert _off(*_long_gate(mhc, 300, C, F32)) < 2.1 * FP32_SUM, C
     for got, ref in _long_weight_grads(mhc, 131072, 1024, 2432, F32):
@@ -487,6 +490,34 @@ def test_long_bf16_sums_of_one_sign(mhc):
         ref = sum(R.ffn(x[:4], wg[f:f + 4096], wu[f:f + 4096], wd[:, f:f + 4096], "silu")
                   for f in range(0, F, 4096))
         assert _off(y, ref) < 2.0 ** -11 + own, T
+
+
+def test_long_bf16_gates_of_one_sign(mhc):
+    """The gate's sums over channels, and those of da: 65536 2^-27 at every length, for few tokens
+    (up to eight parts of 65536) and for many.  a takes that of g (1.1) and of u; dg and du take
+    that of da, and of u or g.  The mean of n roundings to bf16 adds 2^-9 / sqrt(n)."""
+    for T, C in ((300, 65600), (300, 262144), (300, 1048576), (40, 524288), (17, 524296)):
+        assert _off(*_long_gate(mhc, T, C, BF16)) < 2.1 * 2.0 ** -11 + 2.0 ** -9 / (64 * T) ** 0.5
+    for T, C in ((300, 262144), (40, 524288)):
+        p = _positive(C + T)
+        x, gy = ((p(T, C) * 2 * p(1, C)).to(BF16) for _ in range(2))
+        wg, wu, wd = (p(64, C) * 4 / C).to(BF16), (p(64, C) * 4 / C).to(BF16), p(C, 64).to(BF16)
+        got = mhc.mhc_ffn_backward(x, wg, wu, wd, gy)
+        ref = R.ffn_grad(x, wg, wu, wd, gy, "silu")
+        for g, r, name in zip(got, ref, GRADS):
+            assert _off(g, r) < 2.2 * 2.0 ** -11 + 2.0 ** -9 / 8192 ** 0.5, (T, C, name)
+
+
+@pytest.mark.parametrize("T,C,F", [(300, 65600, 72), (700, 131080, 200), (129, 524296, 64),
+                                   (5, 64, 262152)])
+def test_sums_of_either_sign_over_many_channels(mhc, T, C, F):
+    """Beyond 65536 channels (and, for few tokens, 2^19 or 2^18 hidden units)."""
+    x, wg, wu, wd, gy = _case(T, C, F, BF16, 21)
+    for act in ("silu", "gelu"):
+        assert R.norm_rel(mhc.mhc_ffn(x, wg, wu, wd, act=act), R.ffn(x, wg, wu, wd, act)) < 2.0 ** -7
+        ref = R.ffn_grad(x, wg, wu, wd, gy, act)
+        for g, r, name in zip(mhc.mhc_ffn_backward(x, wg, wu, wd, gy, act=act), ref, GRADS):
+            assert R.norm_rel(g, r) < 2.0 ** -7, name
 
 
 def test_few_token_fp32_sums_of_one_sign(mhc):
