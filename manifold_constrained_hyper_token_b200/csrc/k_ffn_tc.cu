@@ -769,8 +769,9 @@ cudaError_t launch_tn(GemmArgs& P, const Opnds& o, cudaStream_t s) {
 // bf16 sums of any number of tiles are split where they are longer than kLongSum:
 // they stay in one accumulator, whose adder cuts, and a sum of one sign is off by
 // 2^-11.8 of itself at 65536 k, a sixth of its rounding to bf16 (2^-8.2 at 2^19; fp32
-// sums leave the accumulator on their way).  The parts' fp32 planes are less than a
-// tenth of what g, u, dg, du and a take at such a length.
+// sums leave the accumulator on their way).  The weight gradients' parts take 12 C bytes
+// per hidden unit each, where g, u, dg, du and a take 14 T: a fifth at C = 7168.  T =
+// 98304, C = F = 2048 backward: 5.64 ms, 5.56 without the split.
 struct Plan {
   int tn, split;
 };
