@@ -170,6 +170,20 @@ def test_rows_of_nearly_one_value(mhc, T, C, dtype, value):
     ref = R.norm(x, w, b, 1e-6)
     bound = w.double() * dxh + 4 * R.U * (ref.abs() + b.double().abs())
     R.assert_within(y, ref, bound + R.HALF_STEP[dtype] * (ref.abs() + bound), "y")
+    # backward: the same xh in grad_weight, and in grad_x beside its own sums (64 u each)
+    gy = torch.randn(T, C, generator=g).to(dtype)
+    gx, gw, gb = mhc.mhc_layer_norm_backward(x.cuda(), w.cuda(), gy.cuda())
+    rx, rw, rb = R.norm_grad(x, w, gy, 1e-6)
+    a = gy.double() * w.double()
+    c1, c2 = a.mean(1, keepdim=True), (a * xh).mean(1, keepdim=True)
+    dc1 = 64 * R.U * a.abs().mean(1, keepdim=True)
+    dc2 = (64 * R.U * (a * xh).abs() + a.abs() * dxh).mean(1, keepdim=True)
+    bx = s * (dc1 + xh.abs() * dc2 + c2.abs() * dxh
+              + (72 * R.U + dm * dm) * (a.abs() + c1.abs() + (xh * c2).abs()))
+    R.assert_within(gx, rx, bx + R.HALF_STEP[dtype] * (rx.abs() + bx), "grad_x")
+    ga = gy.double().abs()
+    R.assert_within(gw, rw, (ga * dxh).sum(0) + (T + 16) * R.U * (ga * xh.abs()).sum(0), "grad_w")
+    R.assert_within(gb, rb, (T + 16) * R.U * ga.sum(0), "grad_b")
 
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
