@@ -16,14 +16,15 @@
 // is as large as 1/sqrt(eps) and would make every further rounding of the mean (of
 // a sum, a quotient, or of mean s in x s - mean s) part of the result.  r_w is what
 // is left of the warp's own roundings; in bf16 the sums of such rows are exact and
-// n_w m_w - sum gives it, in fp32 it is added up beside the squares.
+// sum - n_w m_w gives it, in fp32 it is added up beside the squares.
 //
 // With 16 channels per thread and a row at a time the shuffles and joins of a row
 // cost more than its elements (T = 16384, C = 7168 bf16: 187 us forward, 455 us
 // backward).  So a thread takes 32 channels or 64 and, where there are many rows, two
 // rows at a time, in paired fp32 instructions: 98 us (4.8 TB/s) and 173 us (4.1 TB/s;
 // 2 and 6 us of them are the joined mean and x - mean).  What holds them back now is
-// latency: less than half of the issue slots are taken, and most waits are for memory.
+// latency: less than half of the issue slots are taken, most often a warp waits for
+// memory or for its own last result, and there are 14 warps to an SM.
 // The backward's ring leaves an SM two CTAs of 7 warps at that width, and less L1 than
 // the 28 KB of the weight, which is read twice for each pair of rows.
 #include <algorithm>
